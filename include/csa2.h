@@ -63,6 +63,8 @@ extern "C" {
 #define CSA2_MAX_WINDOW 1024     /* largest sliding window */
 #define CSA2_STATIC_SCRATCH_BYTES (4u << 20) /* device array behind csa2_reindex_static */
 #define CSA2_MAX_SHARDS 64       /* largest number of context-parallel shards per merge */
+#define CSA2_BF16 0              /* element types of the 8-bit-cache calls' 16-bit arrays */
+#define CSA2_F16 1
 
 typedef enum csa2_status {
   CSA2_OK = 0,
@@ -75,8 +77,10 @@ typedef enum csa2_status {
 
 /* Bits of the device status word. */
 #define CSA2_DEV_BAD_INDEX 0x1u  /* entry/block index or destination out of range */
-#define CSA2_DEV_BAD_COUNT 0x2u  /* n_vis outside [0, max_n_vis] or past the pool */
+#define CSA2_DEV_BAD_COUNT 0x2u  /* n_vis outside [0, max_n_vis] or past the pool; a length, a
+                                  * query range or a free-list count that cannot be */
 #define CSA2_DEV_TIMEOUT 0x4u    /* bounded wait expired */
+#define CSA2_DEV_NO_PAGES 0x8u   /* the free list of a paged pool ran out */
 
 const char* csa2_status_string(csa2_status s);
 /* Map a device status word (OR of CSA2_DEV_* bits) to a status; 0 -> CSA2_OK. */
@@ -309,6 +313,108 @@ csa2_status csa2_topk_localize(const int32_t* topk, int B, int Q, int K, const i
 csa2_status csa2_attn_combine(const float* out_parts, int64_t out_part_stride, const float* lse_parts,
                               int64_t lse_part_stride, int C, int B, int Q, int H, float* out, float* lse,
                               cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * Paged 8-bit KV cache: the K/V of ordinary attention layers served next to CSA2 layers (a
+ * drafter's, dense or windowed layers; the pages keep such windows in 8 bits, P3 §4비트로
+ * 적어도 되는 이유, and give no layout, so the one below is this library's).
+ *
+ *  - A page holds `page` tokens (16, 32, 64 or 128) of every key head.  k_cache, v_cache: u8
+ *    [n_pages][Hk][page][hd] E4M3 codes, hd 64 or 128; k_scale, v_scale: fp32 [n_pages][Hk],
+ *    one scale per page and head.  Value = scale * E4M3(code).
+ *  - block_table int32 [R][max_pages]: request r's j-th page holds its tokens j*page ..
+ *    j*page + page - 1; -1 where it has none.  A page belongs to one request.
+ *    max_pages * page is at most 2^30.
+ *  - A slot is page_id * page + row (int64, -1 = none).  A batch of R requests brings n_r new
+ *    tokens each, T rows in all, request after request: rows q_start[r] .. q_start[r+1] - 1.
+ *  - One step: csa2_paged_plan, then per layer csa2_kv8_append and csa2_kv8_attn (every layer
+ *    has its own caches and scales; tables and slots are shared); csa2_paged_release when
+ *    requests end.  All of it runs from device arrays, so a step can be captured once in a
+ *    CUDA graph and replayed with new lengths.
+ * --------------------------------------------------------------------------------- */
+
+/* Block tables, slot maps and positions from request lengths.
+ *   ctx_len int32 [R]  tokens each request holds;  new_len int32 [R]  tokens it adds (>= 0)
+ *   block_table  in/out: the pages of the ctx_len tokens must be in it; the new ones are added
+ *   free_pages int32 [free_cap], n_free int32 [1]: a stack, taken from its end; not changed
+ *   seq_len int32 [R] out: ctx_len + new_len (may be ctx_len itself)
+ *   n_free_out int32 [1] out: what is left of the stack (may be n_free itself)
+ *   q_start int32 [R+1] out: first row of each request, and the number of rows
+ *   slot_map, pos int64 [T_cap] out: slot and position of each row; -1 in the rows after the
+ *   last (slot_map is csa2_kv8_append's; pos is csa2_pack_kv_normed's table row)
+ * Pages are given out in the order of the requests, then of the pages: the k-th new page of
+ * the call is free_pages[n_free - 1 - k].  Beyond the stack a request gets -1 entries, its
+ * rows there get slot -1, and CSA2_DEV_NO_PAGES is flagged.  Rows beyond T_cap are cut off
+ * new_len, entries beyond max_pages are not made (their rows get slot -1), negative lengths
+ * count as 0 and n_free is brought into [0, free_cap]: each flags CSA2_DEV_BAD_COUNT.  A page
+ * id outside [0, n_pages) is stored as -1 (slot -1) and flags CSA2_DEV_BAD_INDEX. */
+csa2_status csa2_paged_plan(const int32_t* ctx_len, const int32_t* new_len, int R, int page, int32_t* block_table,
+                            int max_pages, const int32_t* free_pages, int64_t free_cap, const int32_t* n_free,
+                            int64_t n_pages, int32_t* seq_len, int32_t* n_free_out, int32_t* q_start,
+                            int64_t* slot_map, int64_t* pos, int64_t T_cap, uint32_t* dev_status,
+                            cudaStream_t stream);
+
+/* The pages of finished requests back on the stack.
+ *   seq_len int32 [R], block_table int32 [R][max_pages]; release u8 [R]: nonzero = request ends
+ *   free_pages int32 [free_cap] in/out, n_free int32 [1]
+ *   seq_len_out int32 [R]: 0 for ended requests, seq_len for the others (may be seq_len)
+ *   n_free_out int32 [1] (may be n_free)
+ * The ceil(seq_len / page) pages of each ended request are written from free_pages[n_free] on,
+ * in the order of the requests, then of the pages.  Entries outside [0, n_pages) are left out
+ * (CSA2_DEV_BAD_INDEX), pages beyond free_cap are dropped and lengths that are negative or
+ * exceed the table are cut (CSA2_DEV_BAD_COUNT).  block_table is not changed: entries past a
+ * request's length are never read. */
+csa2_status csa2_paged_release(const int32_t* seq_len, const int32_t* block_table, const uint8_t* release, int R,
+                               int page, int max_pages, int32_t* free_pages, int64_t free_cap, const int32_t* n_free,
+                               int64_t n_pages, int32_t* seq_len_out, int32_t* n_free_out, uint32_t* dev_status,
+                               cudaStream_t stream);
+
+/* New keys and values into the cache.
+ *   k, v  16-bit [T][Hk][hd] (dtype CSA2_BF16 or CSA2_F16); k_stride, v_stride: elements from
+ *         one token to the next (0 = Hk*hd; a multiple of 8, so views of a fused projection do)
+ *   slot_map int64 [T]: -1 rows are skipped; the rows of one page are consecutive in the batch
+ *         and their slots ascend by one (csa2_paged_plan's are so)
+ * For every page touched and head, K and V apart: the first row written by the call decides
+ * what is earlier.  With s_new the smallest power of two >= 2^-64 such that |x| <= 448 s_new
+ * for every new x of the page, s = s_new when the call writes the page's row 0, else
+ * max(page's scale, s_new).  Rows before the first written one are re-encoded when s grew:
+ * code' = E4M3_RNE(code * (old / s)) (a power of two: exact but for subnormal codes).  New
+ * rows: code = E4M3_RNE_sat(x / s).  A power of two costs E4M3 no precision, and a page may be
+ * re-scaled any number of times without the rounding adding up.  Output is bit-exact with that
+ * definition.  Slots outside [-1, n_pages*page) and rows that break the order within their
+ * page are skipped and flag CSA2_DEV_BAD_INDEX. */
+csa2_status csa2_kv8_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, int dtype, int64_t T,
+                            int Hk, int hd, const int64_t* slot_map, uint8_t* k_cache, uint8_t* v_cache,
+                            float* k_scale, float* v_scale, int64_t n_pages, int page, uint32_t* dev_status,
+                            cudaStream_t stream);
+
+/* Causal attention of the batch's rows over the cache.
+ *   q   16-bit [T][Hq][hd] (q_stride elements between tokens, 0 = Hq*hd; a multiple of 8);
+ *       query head h reads key head h / (Hq/Hk)
+ *   q_start int32 [R+1], seq_len int32 [R]: row i of request r is its token
+ *       p = seq_len[r] - n_r + i, which sees tokens max(0, p - window + 1) .. p (window 0: 0 .. p)
+ *   max_q  about how many rows a request brings (1 for decode): it picks the tile shape; other
+ *       numbers of rows are right too.  It also sizes the workspace.
+ *   softcap > 0: scores s become softcap * tanh(s / softcap); 0 leaves them
+ *   out 16-bit [T][Hq][hd];  lse fp32 [T][Hq] (natural log; may be NULL)
+ * s = sm_scale * q . (k_scale K), out = softmax(s) (v_scale V).  Both products run on the
+ * tcgen05 tensor cores on the E4M3 codes as stored; the queries enter as E4M3 digits that hold
+ * every bf16 / fp16 value to 2^-22 of its head's largest element, the probabilities rounded to
+ * f16; sums are fp32.  Scales: k_scale finite, v_scale in [0, 2^64].  A row that sees no key
+ * gives out = 0, lse = -inf.  Rows of q outside every request are not read and theirs of out and
+ * lse are left as they were; what the cache holds outside the rows a request sees (any bits,
+ * NaN included) does not matter.  Entries of block_table outside [0, n_pages) among the pages a
+ * request sees are masked and flag CSA2_DEV_BAD_INDEX; lengths that are negative, shorter than
+ * the rows brought, or longer than the table, and q_start outside [0, T] or descending are cut
+ * and flag CSA2_DEV_BAD_COUNT.  Results do not depend on timing: the same call gives the same
+ * bits. */
+size_t csa2_kv8_attn_workspace_size(int Hq, int Hk, int hd, int max_q, int dtype);
+csa2_status csa2_kv8_attn(const void* q, int64_t q_stride, int dtype, int64_t T, int Hq, int Hk, int hd,
+                          const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                          int64_t n_pages, int page, const int32_t* block_table, int max_pages, const int32_t* q_start,
+                          const int32_t* seq_len, int R, int max_q, float sm_scale, int window, float softcap,
+                          void* out, float* lse, void* ws, size_t ws_bytes, uint32_t* dev_status,
+                          cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------------
  * csa2_reindex_static: csa2_reindex without a workspace argument.  The pages have no

@@ -21,6 +21,7 @@ FLAGS = [
     # share the CUDA runtime with the host process (torch), so the current device and
     # streams are the caller's
     "-cudart", "shared",
+    "--threads", "4",
 ]
 
 

@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libcsa2.so")
 CSA2_OK = 0
 STATUS_NAMES = {0: "CSA2_OK", 1: "CSA2_ERR_INVALID_ARG", 2: "CSA2_ERR_UNSUPPORTED", 3: "CSA2_ERR_CUDA",
                 4: "CSA2_ERR_TIMEOUT", 5: "CSA2_ERR_DEVICE_INPUT"}
-DEV_BAD_INDEX, DEV_BAD_COUNT, DEV_TIMEOUT = 0x1, 0x2, 0x4
+DEV_BAD_INDEX, DEV_BAD_COUNT, DEV_TIMEOUT, DEV_NO_PAGES = 0x1, 0x2, 0x4, 0x8
 
 D, DI, KV_BYTES, IK_BYTES = 512, 128, 288, 68
 
@@ -83,6 +83,17 @@ def lib():
         L.csa2_topk_localize.argtypes = [P, I32, I32, I32, P, P, P, P, P]
         L.csa2_attn_combine.restype = I32
         L.csa2_attn_combine.argtypes = [P, I64, P, I64, I32, I32, I32, I32, P, P, P]
+        L.csa2_paged_plan.restype = I32
+        L.csa2_paged_plan.argtypes = [P, P, I32, I32, P, I32, P, I64, P, I64, P, P, P, P, P, I64, P, P]
+        L.csa2_paged_release.restype = I32
+        L.csa2_paged_release.argtypes = [P, P, P, I32, I32, I32, P, I64, P, I64, P, P, P, P]
+        L.csa2_kv8_append.restype = I32
+        L.csa2_kv8_append.argtypes = [P, P, I64, I64, I32, I64, I32, I32, P, P, P, P, P, I64, I32, P, P]
+        L.csa2_kv8_attn_workspace_size.restype = SZ
+        L.csa2_kv8_attn_workspace_size.argtypes = [I32, I32, I32, I32, I32]
+        L.csa2_kv8_attn.restype = I32
+        L.csa2_kv8_attn.argtypes = [P, I64, I32, I64, I32, I32, I32, P, P, P, P, I64, I32, P, I32, P, P, I32, I32, F32,
+                                    I32, F32, P, P, P, SZ, P, P]
         _lib = L
     return _lib
 
@@ -491,3 +502,171 @@ def csa2_attn_combine(out_parts, lse_parts, out, lse, stream=None):
     _need(lse, torch.float32, "lse", 3)
     _check(lib().csa2_attn_combine(_ptr(out_parts), int(pso), _ptr(lse_parts), int(psl), C, B, Q, H, _ptr(out),
                                    _ptr(lse), _stream(stream)), "csa2_attn_combine")
+
+
+# ---- paged 8-bit KV cache ----------------------------------------------------------------
+_KV_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _arg(t, dtype, shape, name, dev):
+    """Raise unless t is a contiguous `dtype` tensor of exactly `shape` on `dev`; its address."""
+    if not (t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()):
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _tokens(t, dtype, shape, name, dev):
+    """The same for a [T, heads, hd] view whose tokens are each contiguous: (address, token stride)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    row = shape[1] * shape[2]
+    st = t.stride()
+    if shape[0] > 0 and ((st[2] != 1) or (st[1] != shape[2] and shape[1] > 1)):
+        raise ValueError(f"{name}: each token's [heads, hd] must be contiguous")
+    if shape[0] <= 1:
+        return t.data_ptr(), row
+    if st[0] < row or st[0] % 8:
+        raise ValueError(f"{name}: the token stride must be a multiple of 8 elements and at least heads * hd")
+    return t.data_ptr(), st[0]
+
+
+def _flag_arg(dev_status, dev):
+    if dev_status is None:
+        return None
+    if dev_status.dtype is not torch.int32 or dev_status.numel() < 1 or dev_status.device != dev:
+        raise ValueError(f"dev_status must be an int32 tensor with at least one element on {dev}")
+    return dev_status.data_ptr()
+
+
+def _cuda_dev(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _call_on(dev, stream, fn, *args):
+    """fn(*args, stream) with `dev` current (the library launches on the current device)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
+    if torch.cuda.current_device() == dev.index:
+        return fn(*args, stream.cuda_stream)
+    with torch.cuda.device(dev):
+        return fn(*args, stream.cuda_stream)
+
+
+def csa2_paged_plan(ctx_len, new_len, block_table, free_pages, n_free, page, n_pages, seq_len, n_free_out, q_start,
+                    slot_map, pos, dev_status=None, stream=None):
+    """ctx_len, new_len i32 [R], block_table i32 [R,max_pages] (new pages are added),
+    free_pages i32 [F] with n_free i32 [1] valid -> seq_len i32 [R], n_free_out i32 [1],
+    q_start i32 [R+1], slot_map and pos i64 [T_cap] (see include/csa2.h).  seq_len may be
+    ctx_len and n_free_out may be n_free."""
+    dev = _cuda_dev(ctx_len, "ctx_len")
+    _shape(ctx_len, (None,), "ctx_len")
+    _shape(block_table, (ctx_len.shape[0], None), "block_table")
+    _shape(free_pages, (None,), "free_pages")
+    _shape(slot_map, (None,), "slot_map")
+    R, T, i32, i64 = ctx_len.shape[0], slot_map.shape[0], torch.int32, torch.int64
+    _check(_call_on(
+        dev, stream, lib().csa2_paged_plan, _arg(ctx_len, i32, (R,), "ctx_len", dev),
+        _arg(new_len, i32, (R,), "new_len", dev), R, page,
+        _arg(block_table, i32, block_table.shape, "block_table", dev), block_table.shape[1],
+        _arg(free_pages, i32, free_pages.shape, "free_pages", dev), free_pages.shape[0],
+        _arg(n_free, i32, (1,), "n_free", dev), n_pages, _arg(seq_len, i32, (R,), "seq_len", dev),
+        _arg(n_free_out, i32, (1,), "n_free_out", dev), _arg(q_start, i32, (R + 1,), "q_start", dev),
+        _arg(slot_map, i64, (T,), "slot_map", dev), _arg(pos, i64, (T,), "pos", dev), T, _flag_arg(dev_status, dev)),
+        "csa2_paged_plan")
+
+
+def csa2_paged_release(seq_len, block_table, release, free_pages, n_free, page, n_pages, seq_len_out, n_free_out,
+                       dev_status=None, stream=None):
+    """The pages of requests whose release u8 [R] is nonzero, pushed onto free_pages i32 [F]
+    after its n_free i32 [1] entries; seq_len_out i32 [R] (0 for those) and n_free_out i32 [1]
+    may be seq_len and n_free."""
+    dev = _cuda_dev(seq_len, "seq_len")
+    _shape(seq_len, (None,), "seq_len")
+    _shape(block_table, (seq_len.shape[0], None), "block_table")
+    _shape(free_pages, (None,), "free_pages")
+    R, i32 = seq_len.shape[0], torch.int32
+    _check(_call_on(
+        dev, stream, lib().csa2_paged_release, _arg(seq_len, i32, (R,), "seq_len", dev),
+        _arg(block_table, i32, block_table.shape, "block_table", dev),
+        _arg(release, torch.uint8, (R,), "release", dev), R, page, block_table.shape[1],
+        _arg(free_pages, i32, free_pages.shape, "free_pages", dev), free_pages.shape[0],
+        _arg(n_free, i32, (1,), "n_free", dev), n_pages, _arg(seq_len_out, i32, (R,), "seq_len_out", dev),
+        _arg(n_free_out, i32, (1,), "n_free_out", dev), _flag_arg(dev_status, dev)), "csa2_paged_release")
+
+
+def _cache_args(k_cache, v_cache, k_scale, v_scale, dev):
+    """(n_pages, Hk, page, hd) and the four addresses of one layer's cache."""
+    _shape(k_cache, (None, None, None, None), "k_cache")
+    sh = k_cache.shape
+    return sh, (_arg(k_cache, torch.uint8, sh, "k_cache", dev), _arg(v_cache, torch.uint8, sh, "v_cache", dev),
+                _arg(k_scale, torch.float32, sh[:2], "k_scale", dev),
+                _arg(v_scale, torch.float32, sh[:2], "v_scale", dev))
+
+
+def csa2_kv8_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, dev_status=None, stream=None):
+    """k, v bf16 or fp16 [T,Hk,hd] (token-strided views allowed) written as E4M3 codes into
+    k_cache, v_cache u8 [n_pages,Hk,page,hd] at slot_map i64 [T], with one power-of-two scale
+    per page and head in k_scale, v_scale f32 [n_pages,Hk] (see include/csa2.h)."""
+    dev = _cuda_dev(k, "k")
+    (P, Hk, page, hd), cache = _cache_args(k_cache, v_cache, k_scale, v_scale, dev)
+    if k.dtype not in _KV_DTYPES:
+        raise TypeError(f"k must be bfloat16 or float16, got {k.dtype}")
+    T = k.shape[0] if k.dim() else 0
+    ka, ks = _tokens(k, k.dtype, (T, Hk, hd), "k", dev)
+    va, vs = _tokens(v, k.dtype, (T, Hk, hd), "v", dev)
+    _check(_call_on(dev, stream, lib().csa2_kv8_append, ka, va, ks, vs, _KV_DTYPES[k.dtype], T, Hk, hd,
+                    _arg(slot_map, torch.int64, (T,), "slot_map", dev), *cache, P, page, _flag_arg(dev_status, dev)),
+           "csa2_kv8_append")
+
+
+def csa2_kv8_attn_workspace_size(Hq, Hk, hd, max_q, dtype=torch.bfloat16):
+    return lib().csa2_kv8_attn_workspace_size(Hq, Hk, hd, max_q, _KV_DTYPES[dtype])
+
+
+def csa2_kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, q_start, seq_len, sm_scale, out, lse=None,
+                  max_q=1, window=0, softcap=0.0, ws=None, dev_status=None, stream=None):
+    """q bf16 or fp16 [T,Hq,hd] (token-strided views allowed), the cache of csa2_kv8_append,
+    block_table i32 [R,max_pages], q_start i32 [R+1], seq_len i32 [R] -> out like q
+    (contiguous) and lse f32 [T,Hq] or None (see include/csa2.h)."""
+    dev = _cuda_dev(q, "q")
+    (P, Hk, page, hd), cache = _cache_args(k_cache, v_cache, k_scale, v_scale, dev)
+    if q.dtype not in _KV_DTYPES:
+        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
+    _shape(q, (None, None, hd), "q")
+    _shape(seq_len, (None,), "seq_len")
+    _shape(block_table, (seq_len.shape[0], None), "block_table")
+    T, Hq, _ = q.shape
+    R, kind = seq_len.shape[0], _KV_DTYPES[q.dtype]
+    qa, qs = _tokens(q, q.dtype, q.shape, "q", dev)
+    L = lib()
+    if ws is None:
+        # taken on the stream that uses it, so the allocator keeps it until the kernels are done
+        need = L.csa2_kv8_attn_workspace_size(Hq, Hk, hd, max_q, kind)
+        if stream is None:
+            ws = workspace(need, dev)
+        else:
+            with torch.cuda.stream(stream):
+                ws = workspace(need, dev)
+    elif ws.dtype is not torch.uint8 or ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
+    _check(_call_on(
+        dev, stream, L.csa2_kv8_attn, qa, qs, kind, T, Hq, Hk, hd, *cache, P, page,
+        _arg(block_table, torch.int32, block_table.shape, "block_table", dev), block_table.shape[1],
+        _arg(q_start, torch.int32, (R + 1,), "q_start", dev), _arg(seq_len, torch.int32, (R,), "seq_len", dev), R,
+        max_q, sm_scale, window, softcap, _arg(out, q.dtype, (T, Hq, hd), "out", dev),
+        None if lse is None else _arg(lse, torch.float32, (T, Hq), "lse", dev), ws.data_ptr(), ws.numel(),
+        _flag_arg(dev_status, dev)), "csa2_kv8_attn")

@@ -37,6 +37,24 @@ cudaError_t launch_topk_localize(const int32_t* topk, int B, int Q, int K, const
                                  int32_t* out, uint32_t* status, cudaStream_t stream);
 cudaError_t launch_attn_combine(const float* out_parts, int64_t part_o, const float* lse_parts, int64_t part_l,
                                 int C, int64_t N, float* out, float* lse, cudaStream_t stream);
+cudaError_t launch_paged_plan(const int32_t* ctx_len, const int32_t* new_len, int R, int page, int32_t* table,
+                              int max_pages, const int32_t* free_pages, int64_t free_cap, const int32_t* n_free,
+                              int64_t n_pages, int32_t* seq_len, int32_t* n_free_out, int32_t* q_start,
+                              int64_t* slot_map, int64_t* pos, int64_t t_cap, uint32_t* status, cudaStream_t stream);
+cudaError_t launch_paged_release(const int32_t* seq_len, const int32_t* table, const uint8_t* release, int R,
+                                 int page, int max_pages, int32_t* free_pages, int64_t free_cap,
+                                 const int32_t* n_free, int64_t n_pages, int32_t* seq_len_out, int32_t* n_free_out,
+                                 uint32_t* status, cudaStream_t stream);
+cudaError_t launch_kv8_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, int f16, int64_t T,
+                              int Hk, int hd, const int64_t* slot, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,
+                              float* v_scale, int64_t n_pages, int page, uint32_t* status, cudaStream_t stream,
+                              int num_sms);
+size_t kv8_attn_workspace_bytes(int Hq, int Hk, int hd, int max_q, int f16, int num_sms);
+cudaError_t launch_kv8_attn(const void* q, int64_t q_stride, int f16, int64_t T, int Hq, int Hk, int hd,
+                            const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                            int64_t n_pages, int page, const int32_t* table, int max_pages, const int32_t* q_start,
+                            const int32_t* seq_len, int R, int max_q, float sm_scale, int window, float softcap,
+                            void* out, float* lse, void* ws, uint32_t* status, cudaStream_t stream, int num_sms);
 }  // namespace csa2
 
 namespace {
@@ -103,11 +121,11 @@ const char* csa2_status_string(csa2_status s) {
 
 csa2_status csa2_status_from_device_word(uint32_t word) {
   if (word & CSA2_DEV_TIMEOUT) return CSA2_ERR_TIMEOUT;
-  if (word & (CSA2_DEV_BAD_INDEX | CSA2_DEV_BAD_COUNT)) return CSA2_ERR_DEVICE_INPUT;
+  if (word & (CSA2_DEV_BAD_INDEX | CSA2_DEV_BAD_COUNT | CSA2_DEV_NO_PAGES)) return CSA2_ERR_DEVICE_INPUT;
   return CSA2_OK;
 }
 
-int csa2_version(void) { return 100; }
+int csa2_version(void) { return 200; }
 
 csa2_status csa2_pack_kv(const void* kv, const void* ik, int64_t T, int ratio,
                          const int64_t* dst_entry, int64_t pool_entries, uint8_t* kv_pool,
@@ -364,6 +382,130 @@ csa2_status csa2_attn_combine(const float* out_parts, int64_t out_part_stride, c
   if (!aligned(out_parts, 16) || !aligned(lse_parts, 4) || !aligned(out, 16) || !aligned(lse, 4))
     return CSA2_ERR_INVALID_ARG;
   return launched(csa2::launch_attn_combine(out_parts, part_o, lse_parts, part_l, C, N, out, lse, stream));
+}
+
+// ---- paged 8-bit KV cache ----------------------------------------------------------------
+
+namespace {
+
+bool valid_page(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+constexpr int64_t kMaxRows = (int64_t)1 << 31;   // rows of hd bytes in one cache (a copy's coordinate is int32)
+constexpr int64_t kMaxHeld = (int64_t)1 << 30;   // tokens a block-table row can name
+
+// Checks shared by the calls that take a block table.
+csa2_status check_table(int R, int page, const void* table, int max_pages, int64_t n_pages) {
+  if (!valid_page(page)) return CSA2_ERR_UNSUPPORTED;
+  if (R < 0 || max_pages < 1 || n_pages < 0) return CSA2_ERR_INVALID_ARG;
+  if ((int64_t)max_pages * page > kMaxHeld || n_pages > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
+  if (R > 0 && (!table || !aligned(table, 4))) return CSA2_ERR_INVALID_ARG;
+  return CSA2_OK;
+}
+
+// Checks shared by the calls that take the cache; hd, page and the head count of a row of it.
+csa2_status check_cache(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                        int64_t n_pages, int page, int Hk, int hd) {
+  if (!valid_page(page) || (hd != 64 && hd != 128)) return CSA2_ERR_UNSUPPORTED;
+  if (Hk < 1 || n_pages < 1) return CSA2_ERR_INVALID_ARG;
+  if (n_pages > INT32_MAX || n_pages * page > (kMaxRows - 1) / Hk) return CSA2_ERR_UNSUPPORTED;
+  if (!k_cache || !v_cache || !k_scale || !v_scale) return CSA2_ERR_INVALID_ARG;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+    return CSA2_ERR_INVALID_ARG;
+  return CSA2_OK;
+}
+
+}  // namespace
+
+csa2_status csa2_paged_plan(const int32_t* ctx_len, const int32_t* new_len, int R, int page, int32_t* block_table,
+                            int max_pages, const int32_t* free_pages, int64_t free_cap, const int32_t* n_free,
+                            int64_t n_pages, int32_t* seq_len, int32_t* n_free_out, int32_t* q_start,
+                            int64_t* slot_map, int64_t* pos, int64_t T_cap, uint32_t* dev_status,
+                            cudaStream_t stream) {
+  csa2_status st = check_table(R, page, block_table, max_pages, n_pages);
+  if (st != CSA2_OK) return st;
+  if (free_cap < 0 || T_cap < 0) return CSA2_ERR_INVALID_ARG;
+  if (free_cap > INT32_MAX || T_cap > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
+  if (!n_free || !n_free_out || !q_start || !aligned(n_free, 4) || !aligned(n_free_out, 4) || !aligned(q_start, 4))
+    return CSA2_ERR_INVALID_ARG;
+  if (R > 0 && (!ctx_len || !new_len || !seq_len || !aligned(ctx_len, 4) || !aligned(new_len, 4) ||
+                !aligned(seq_len, 4) || seq_len == new_len))
+    return CSA2_ERR_INVALID_ARG;
+  if (free_cap > 0 && (!free_pages || !aligned(free_pages, 4))) return CSA2_ERR_INVALID_ARG;
+  if (T_cap > 0 && (!slot_map || !pos || !aligned(slot_map, 8) || !aligned(pos, 8))) return CSA2_ERR_INVALID_ARG;
+  if (dev_status && !aligned(dev_status, 4)) return CSA2_ERR_INVALID_ARG;
+  return launched(csa2::launch_paged_plan(ctx_len, new_len, R, page, block_table, max_pages, free_pages, free_cap,
+                                          n_free, n_pages, seq_len, n_free_out, q_start, slot_map, pos, T_cap,
+                                          dev_status, stream));
+}
+
+csa2_status csa2_paged_release(const int32_t* seq_len, const int32_t* block_table, const uint8_t* release, int R,
+                               int page, int max_pages, int32_t* free_pages, int64_t free_cap, const int32_t* n_free,
+                               int64_t n_pages, int32_t* seq_len_out, int32_t* n_free_out, uint32_t* dev_status,
+                               cudaStream_t stream) {
+  csa2_status st = check_table(R, page, block_table, max_pages, n_pages);
+  if (st != CSA2_OK) return st;
+  if (free_cap < 0) return CSA2_ERR_INVALID_ARG;
+  if (free_cap > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
+  if (!n_free || !n_free_out || !aligned(n_free, 4) || !aligned(n_free_out, 4)) return CSA2_ERR_INVALID_ARG;
+  if (R > 0 && (!seq_len || !seq_len_out || !release || !aligned(seq_len, 4) || !aligned(seq_len_out, 4)))
+    return CSA2_ERR_INVALID_ARG;
+  if (free_cap > 0 && (!free_pages || !aligned(free_pages, 4))) return CSA2_ERR_INVALID_ARG;
+  if (dev_status && !aligned(dev_status, 4)) return CSA2_ERR_INVALID_ARG;
+  return launched(csa2::launch_paged_release(seq_len, block_table, release, R, page, max_pages, free_pages, free_cap,
+                                             n_free, n_pages, seq_len_out, n_free_out, dev_status, stream));
+}
+
+csa2_status csa2_kv8_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, int dtype, int64_t T,
+                            int Hk, int hd, const int64_t* slot_map, uint8_t* k_cache, uint8_t* v_cache,
+                            float* k_scale, float* v_scale, int64_t n_pages, int page, uint32_t* dev_status,
+                            cudaStream_t stream) {
+  csa2_status st = check_cache(k_cache, v_cache, k_scale, v_scale, n_pages, page, Hk, hd);
+  if (st != CSA2_OK) return st;
+  if (dtype != CSA2_BF16 && dtype != CSA2_F16) return CSA2_ERR_UNSUPPORTED;
+  if (T < 0 || k_stride < 0 || v_stride < 0) return CSA2_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)Hk * hd;
+  k_stride = k_stride ? k_stride : row;
+  v_stride = v_stride ? v_stride : row;
+  if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8) return CSA2_ERR_INVALID_ARG;
+  if (T == 0) return CSA2_OK;
+  if (T > INT32_MAX / Hk) return CSA2_ERR_UNSUPPORTED;
+  if (!k || !v || !slot_map || !aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 8)) return CSA2_ERR_INVALID_ARG;
+  if (dev_status && !aligned(dev_status, 4)) return CSA2_ERR_INVALID_ARG;
+  return launched(csa2::launch_kv8_append(k, v, k_stride, v_stride, dtype == CSA2_F16, T, Hk, hd, slot_map, k_cache,
+                                          v_cache, k_scale, v_scale, n_pages, page, dev_status, stream,
+                                          current_sm_count()));
+}
+
+size_t csa2_kv8_attn_workspace_size(int Hq, int Hk, int hd, int max_q, int dtype) {
+  if (Hk < 1 || Hq < Hk || Hq % Hk || (hd != 64 && hd != 128) || (dtype != CSA2_BF16 && dtype != CSA2_F16)) return 0;
+  return round256(csa2::kv8_attn_workspace_bytes(Hq, Hk, hd, max_q, dtype == CSA2_F16, current_sm_count()));
+}
+
+csa2_status csa2_kv8_attn(const void* q, int64_t q_stride, int dtype, int64_t T, int Hq, int Hk, int hd,
+                          const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                          int64_t n_pages, int page, const int32_t* block_table, int max_pages, const int32_t* q_start,
+                          const int32_t* seq_len, int R, int max_q, float sm_scale, int window, float softcap,
+                          void* out, float* lse, void* ws, size_t ws_bytes, uint32_t* dev_status,
+                          cudaStream_t stream) {
+  csa2_status st = check_cache(k_cache, v_cache, k_scale, v_scale, n_pages, page, Hk, hd);
+  if (st != CSA2_OK) return st;
+  if ((st = check_table(R, page, block_table, max_pages, n_pages)) != CSA2_OK) return st;
+  if (dtype != CSA2_BF16 && dtype != CSA2_F16) return CSA2_ERR_UNSUPPORTED;
+  if (Hq < Hk || Hq % Hk || T < 0 || q_stride < 0 || max_q < 1 || window < 0) return CSA2_ERR_INVALID_ARG;
+  if (!std::isfinite(sm_scale) || !std::isfinite(softcap) || softcap < 0.0f) return CSA2_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)Hq * hd;
+  q_stride = q_stride ? q_stride : row;
+  if (q_stride < row || q_stride % 8) return CSA2_ERR_INVALID_ARG;
+  if (T == 0 || R == 0) return CSA2_OK;
+  if (T > INT32_MAX / Hq) return CSA2_ERR_UNSUPPORTED;
+  if (!q || !q_start || !seq_len || !out) return CSA2_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(q_start, 4) || !aligned(seq_len, 4) || (lse && !aligned(lse, 4)))
+    return CSA2_ERR_INVALID_ARG;
+  if (dev_status && !aligned(dev_status, 4)) return CSA2_ERR_INVALID_ARG;
+  if ((st = check_ws(ws, ws_bytes, csa2_kv8_attn_workspace_size(Hq, Hk, hd, max_q, dtype))) != CSA2_OK) return st;
+  return launched(csa2::launch_kv8_attn(q, q_stride, dtype == CSA2_F16, T, Hq, Hk, hd, k_cache, v_cache, k_scale,
+                                        v_scale, n_pages, page, block_table, max_pages, q_start, seq_len, R, max_q,
+                                        sm_scale, window, softcap, out, lse, ws, dev_status, stream,
+                                        current_sm_count()));
 }
 
 }  // extern "C"

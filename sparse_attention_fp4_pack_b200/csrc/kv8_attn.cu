@@ -1,0 +1,1124 @@
+// Attention over the paged 8-bit KV cache (csa2_kv8_attn), on the sm_100a tensor cores.
+//
+// Both products run as tcgen05.mma kind::f8f6f4 with the cache's E4M3 codes as the A operand,
+// exactly as TMA brings them from their pages: nothing is dequantised.  The 16-bit operand of
+// each product is written as a sum of E4M3 digits with weights 1, 1/16, 1/256 instead:
+//   * a query row times a power of two that brings its largest element into [128, 256): two
+//     digits hold every bf16 value (8 significant bits) and three every fp16 value (11)
+//     exactly, down to 2^-22 of the row's largest element;
+//   * a probability (at most 2^8 after its shift) is rounded to f16, which three digits hold
+//     exactly.
+// Digits are extra columns of the same product (N), so they cost no extra reads of the keys.
+// A page's scale multiplies the score of its keys (K) and the probability of its keys (V):
+// exp2(t) with t = score * log2 e + log2(v_scale) is the weight of the key's V codes, and
+// exp2(t) / v_scale its share of the softmax sum, so one running maximum (of t) bounds both.
+//
+// S^T[128 keys x N] = K_tile . Q^T, O^T[hd x N] += V_tile^T . P^T.  Keys are the M rows (TMEM
+// lanes), a column is one (query, head of the group); up to NC columns share a tile's keys.
+// The work of the whole call is one list of key tiles: requests, key heads, column blocks, and
+// the tiles each block sees.  CTA c takes the c-th of equal shares of it; an item cut by a
+// share's border leaves partial sums in the workspace and kv8_merge_kernel joins them.
+//
+// Roles: warps 0-3 (0-7 with 64 columns) softmax, then one producer warp (TMA, page ids,
+// scales) and one warp that issues the products.  Every wait is bounded: on expiry the CTA
+// flags CSA2_DEV_TIMEOUT, drains its copies and products, frees its tensor memory and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+#include <type_traits>
+
+#include "csa2_device.cuh"
+#include "kv8.cuh"
+#include "tc.cuh"
+
+namespace csa2 {
+
+constexpr int kKeys = 128;             // keys per tile = UMMA M
+constexpr int kMaxTilePages = 8;       // pages of 16 rows
+constexpr float kLift = 6.0f;          // probabilities are 2^(t - max + 6), at most 2^8
+constexpr float kSlack = 2.0f;         // the running maximum is raised when exceeded by more (base 2)
+constexpr uint32_t kKvPolls = 1u << 22;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__host__ __device__ constexpr int round16(int n) { return (n + 15) / 16 * 16; }
+constexpr uint32_t pow2_cols(int n) { return n <= 32 ? 32u : n <= 64 ? 64u : n <= 128 ? 128u : n <= 256 ? 256u : 512u; }
+
+struct KvAttnArgs {
+  const uint8_t* q;
+  int64_t q_stride;  // bytes from token to token
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* table;
+  const int32_t* q_start;
+  const int32_t* seq_len;
+  int R, Hq, Hk, max_pages, page_log2;
+  int64_t n_pages;
+  int64_t T;
+  float sm_scale;
+  int window;
+  float softcap;
+  uint8_t* out;
+  float* lse;
+  float* part;    // [CTA][2][NC][hd + 2]
+  int32_t* meta;  // [CTA][8]
+  uint32_t* status;
+};
+
+// Partial results of CTA c: slot 0 the piece that continues an item, slot 1 the one that
+// starts an item and does not end it.  meta: [0] slot 0 (0 none, 1 goes on, 2 ends the item),
+// [1] slot 1 used, [2..5] its request, head, head block, query block.
+constexpr int kMetaInts = 8;
+
+template <int HD, int NC_, int DQ_, bool CAP_>
+struct KvCfg {
+  static constexpr int kHD = HD, NC = NC_, DQ = DQ_;
+  static constexpr bool CAP = CAP_;
+  static constexpr int NS = round16(NC * DQ);   // columns of S
+  static constexpr int NP = round16(NC * 3);    // columns of O
+  static constexpr int kGroups = NC == 64 ? 2 : 1;  // softmax warpgroups
+  static constexpr int CW = NC / kGroups;           // columns per softmax thread
+  static constexpr int kSoft = 128 * kGroups;
+  static constexpr int kThreads = kSoft + 64;
+  static constexpr uint32_t kTile = kKeys * HD;  // bytes of a K or V tile
+  static constexpr uint32_t kQBytes = (NS * HD + 1023) / 1024 * 1024;
+  static constexpr uint32_t kPBytes = NP * kKeys;
+  static constexpr int kCtas = NC <= 16 ? 2 : 1;  // per SM
+  static constexpr uint32_t kBudget = (kCtas == 2 ? 112u : 224u) * 1024u - 4096u;
+  static constexpr int kFit = (int)((kBudget - kQBytes - kPBytes) / (2 * kTile));
+  static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  static constexpr uint32_t kOffK = 0, kOffV = kStages * kTile, kOffQ = 2 * kStages * kTile, kOffP = kOffQ + kQBytes;
+  static constexpr uint32_t kSmem = kOffP + kPBytes + 1024;  // + alignment slack
+  static constexpr uint32_t kColS = 0, kColO = 2 * NS;
+  static constexpr uint32_t kCols = pow2_cols(2 * NS + NP);
+  static constexpr uint32_t kSwz = tc::swizzle_code(HD);
+};
+
+// ---- primitives ------------------------------------------------------------------------
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(map), "r"(0), "r"(row), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
+  if constexpr (N == 8) tc::tmem_ld8(addr, r);
+  else if constexpr (N == 16) tc::tmem_ld16(addr, r);
+  else tc::tmem_ld32(addr, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[N]) {
+  if constexpr (N == 8) tc::tmem_st8_nowait(addr, r);
+  else if constexpr (N == 16) tc::tmem_st16_nowait(addr, r);
+  else tc::tmem_st32_nowait(addr, r);
+}
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+// N values per lane -> lane i holds value i mod N reduced over the warp (N - 1 exchanges, then
+// the remaining whole-warp ones).
+template <int N, bool kMax>
+__device__ __forceinline__ float warp_columns(float (&v)[N], int lane) {
+#pragma unroll
+  for (int n = N / 2; n >= 1; n >>= 1) {
+    const bool upper = (lane & n) != 0;
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const float send = upper ? v[j] : v[j + n];
+      const float keep = upper ? v[j + n] : v[j];
+      const float recv = __shfl_xor_sync(0xffffffffu, send, n);
+      v[j] = kMax ? fmaxf(keep, recv) : keep + recv;
+    }
+  }
+  float x = v[0];
+#pragma unroll
+  for (int o = N; o <= 16; o <<= 1) {
+    const float y = __shfl_xor_sync(0xffffffffu, x, o);
+    x = kMax ? fmaxf(x, y) : x + y;
+  }
+  return x;
+}
+
+// Two probabilities (f16x2) -> three digits each (two bytes per digit), exactly p = d0 + d1/16
+// + d2/256 while p is a normal f16 of at most 2^8.
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)b));
+  return r;
+}
+__device__ __forceinline__ uint32_t rest16(uint32_t p, uint32_t d) {  // (p - d) * 16, exact
+  const __half2 r = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&p), *reinterpret_cast<__half2*>(&d)),
+                            __floats2half2_rn(16.0f, 16.0f));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// ---- the list of key tiles -------------------------------------------------------------
+struct Request {
+  int q0, n;     // first query row, queries
+  int pos0;      // position of the first query
+  int cap;       // keys: min(seq_len, what the table holds)
+  int nqb;       // query blocks
+};
+struct Shape {   // how a request's columns are cut
+  int G, QB, HB, nhb;
+};
+template <int NC>
+__device__ __forceinline__ Shape shape_of(const KvAttnArgs& a) {
+  Shape s;
+  s.G = a.Hq / a.Hk;
+  s.HB = s.G < NC ? s.G : NC;
+  s.QB = s.G < NC ? NC / s.G : 1;
+  s.nhb = (s.G + NC - 1) / NC;
+  return s;
+}
+__device__ __forceinline__ Request request_of(const KvAttnArgs& a, const Shape& s, int r, uint32_t* bad) {
+  Request x;
+  const int64_t b = a.q_start[r], e = a.q_start[r + 1];
+  int len = a.seq_len[r];
+  const int64_t q0 = b < 0 ? 0 : (b < a.T ? b : a.T), q1 = e < q0 ? q0 : (e < a.T ? e : a.T);
+  if (q0 != b || q1 != e || len < 0) *bad |= CSA2_DEV_BAD_COUNT;
+  if (len < 0) len = 0;
+  x.q0 = (int)q0;
+  x.n = (int)(q1 - q0);
+  if (x.n > len) *bad |= CSA2_DEV_BAD_COUNT;
+  x.pos0 = len - x.n;
+  const int64_t held = (int64_t)a.max_pages << a.page_log2;
+  if (len > held) *bad |= CSA2_DEV_BAD_COUNT;
+  x.cap = len < held ? len : (int)held;
+  x.nqb = (x.n + s.QB - 1) / s.QB;
+  return x;
+}
+// Keys [lo, hi) that any query of block qb sees, and its first tile and number of tiles (at
+// least one: a block that sees nothing still writes its rows).
+struct Range {
+  int lo, hi, tile, tiles;
+};
+__device__ __forceinline__ Range range_of(const KvAttnArgs& a, const Shape& s, const Request& x, int qb) {
+  Range g;
+  const int i0 = qb * s.QB, i1 = i0 + s.QB < x.n ? i0 + s.QB : x.n;
+  const int64_t hi = (int64_t)x.pos0 + i1;
+  g.hi = hi < 0 ? 0 : (hi < x.cap ? (int)hi : x.cap);
+  const int64_t lo = a.window > 0 ? (int64_t)x.pos0 + i0 + 1 - a.window : 0;
+  g.lo = lo < 0 ? 0 : (lo < g.hi ? (int)lo : g.hi);
+  g.tile = g.lo / kKeys;
+  const int end = (g.hi + kKeys - 1) / kKeys;
+  g.tiles = end > g.tile ? end - g.tile : 1;
+  return g;
+}
+// Tiles of one (request, key head, head block).
+__device__ __forceinline__ int64_t row_tiles(const KvAttnArgs& a, const Shape& s, const Request& x, int first, int step) {
+  int64_t n = 0;
+  for (int qb = first; qb < x.nqb; qb += step) n += range_of(a, s, x, qb).tiles;
+  return n;
+}
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// row_tiles of request r for each lane (r < R where live), long requests by the whole warp.
+__device__ __forceinline__ int64_t lane_row_tiles(const KvAttnArgs& a, const Shape& s, int r, bool live, int lane,
+                                                  uint32_t* bad) {
+  Request x = {};
+  if (live) x = request_of(a, s, r, bad);
+  const bool big = x.nqb > 8;
+  int64_t n = big ? 0 : row_tiles(a, s, x, 0, 1);
+  unsigned todo = __ballot_sync(0xffffffffu, big);
+  while (todo) {
+    const int src = __ffs(todo) - 1;
+    todo &= todo - 1;
+    Request y;
+    y.q0 = __shfl_sync(0xffffffffu, x.q0, src);
+    y.n = __shfl_sync(0xffffffffu, x.n, src);
+    y.pos0 = __shfl_sync(0xffffffffu, x.pos0, src);
+    y.cap = __shfl_sync(0xffffffffu, x.cap, src);
+    y.nqb = __shfl_sync(0xffffffffu, x.nqb, src);
+    const int64_t m = warp_sum(row_tiles(a, s, y, lane, 32));
+    if (lane == src) n = m;
+  }
+  return n;
+}
+
+// This CTA's share of the list: its length, and where it begins.
+struct Share {
+  int64_t left;
+  int r, hh, qb, off;  // request, key head * nhb + head block, query block, tile inside the item
+};
+
+// A walk over a share's pieces; every role keeps its own.
+struct Walk {
+  int64_t left;
+  int r, hh, qb, off;
+  Request x;
+  Range g;
+  int take;        // tiles of this piece
+  bool first, last;
+  __device__ __forceinline__ void open(const KvAttnArgs& a, const Shape& s) {
+    g = range_of(a, s, x, qb);
+    const int rest = g.tiles - off;
+    take = left < rest ? (int)left : rest;
+    first = off == 0;
+    last = off + take == g.tiles;
+  }
+  __device__ __forceinline__ void start(const KvAttnArgs& a, const Shape& s, const Share& w) {
+    left = w.left;
+    r = w.r;
+    hh = w.hh;
+    qb = w.qb;
+    off = w.off;
+    if (left <= 0) return;
+    uint32_t bad = 0;
+    x = request_of(a, s, r, &bad);
+    open(a, s);
+  }
+  __device__ __forceinline__ void next(const KvAttnArgs& a, const Shape& s) {
+    left -= take;
+    off = 0;
+    if (left <= 0) return;
+    if (++qb < x.nqb) {
+      open(a, s);
+      return;
+    }
+    qb = 0;
+    if (++hh < a.Hk * s.nhb) {
+      open(a, s);
+      return;
+    }
+    hh = 0;
+    uint32_t bad = 0;
+    do {
+      if (++r >= a.R) {  // cannot happen while left > 0
+        left = 0;
+        return;
+      }
+      x = request_of(a, s, r, &bad);
+    } while (x.n == 0);
+    open(a, s);
+  }
+};
+
+// Computed by the whole CTA (kThreads threads); `sums` holds a value per thread.
+template <int kThreads>
+__device__ void find_share(const KvAttnArgs& a, const Shape& s, int64_t* sums, Share* out, uint32_t* bad) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int per = (a.R + kThreads - 1) / kThreads;  // requests per thread, consecutive
+  const int heads = a.Hk * s.nhb;
+  int64_t mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int r = tid * per + i;
+    mine += lane_row_tiles(a, s, r, r < a.R, lane, bad);
+  }
+  sums[tid] = mine * heads;
+  __syncthreads();
+  if (tid < 32) {
+    constexpr int kEach = kThreads / 32;
+    int64_t part = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) part += sums[lane * kEach + i];
+    int64_t upto = part;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+    const int64_t c = blockIdx.x, C = gridDim.x;
+    const int64_t t0 = total / C * c + total % C * c / C, t1 = total / C * (c + 1) + total % C * (c + 1) / C;
+    Share w = {t1 - t0, 0, 0, 0, 0};
+    if (w.left > 0) {
+      // the thread whose requests hold tile t0 ...
+      const unsigned m = __ballot_sync(0xffffffffu, upto > t0);
+      const int l0 = __ffs(m) - 1;
+      int64_t before = __shfl_sync(0xffffffffu, upto - part, l0);
+      int th = l0 * kEach;
+      while (before + sums[th] <= t0) before += sums[th++];
+      // ... the request (32 at a time) ...
+      int64_t rest = t0 - before;
+      int r = th * per;
+      Request x;
+      int64_t row;
+      for (;;) {
+        const int64_t n = lane_row_tiles(a, s, r + lane, r + lane < a.R, lane, bad) * heads;
+        int64_t in = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, in, o);
+          if (lane >= o) in += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, in > rest);
+        if (hit) {
+          const int l = __ffs(hit) - 1;
+          rest -= __shfl_sync(0xffffffffu, in - n, l);
+          row = __shfl_sync(0xffffffffu, n, l) / heads;
+          r += l;
+          break;
+        }
+        rest -= __shfl_sync(0xffffffffu, in, 31);
+        r += 32;
+      }
+      x = request_of(a, s, r, bad);
+      w.r = r;
+      w.hh = (int)(rest / row);
+      rest -= (int64_t)w.hh * row;
+      // ... and the query block
+      for (int qb0 = 0;; qb0 += 32) {
+        const int n = qb0 + lane < x.nqb ? range_of(a, s, x, qb0 + lane).tiles : 0;
+        int64_t in = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, in, o);
+          if (lane >= o) in += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, in > rest);
+        if (hit) {
+          const int l = __ffs(hit) - 1;
+          w.qb = qb0 + l;
+          w.off = (int)(rest - __shfl_sync(0xffffffffu, in - n, l));
+          break;
+        }
+        rest -= __shfl_sync(0xffffffffu, in, 31);
+        if (qb0 + 32 >= x.nqb) break;  // cannot happen
+      }
+    }
+    if (lane == 0) *out = w;
+  }
+  __syncthreads();
+}
+
+// ---- shared state of a CTA -----------------------------------------------------------------
+template <class C>
+struct KvShared {
+  uint64_t kfull[C::kStages], kempty[C::kStages], vfull[C::kStages], vempty[C::kStages];
+  uint64_t sfull[2], sfree[2], qfull, pfull, pvdone, drain;
+  uint32_t tmem;
+  int abort;
+  Share share;
+  int64_t sums[C::kThreads];
+  float ks[C::kStages][kMaxTilePages], vs[C::kStages][kMaxTilePages];
+  float qscale[C::NC];
+  int col_lo[C::NC], col_hi[C::NC];
+  int64_t col_row[C::NC];  // row of out / lse (token * Hq + head), -1 for padding columns
+  float red[C::kGroups][4][C::CW];
+  float linv[C::NC];
+};
+
+// Bounded wait that also ends when another role has given up.
+template <class C>
+__device__ __forceinline__ bool kv_wait(KvShared<C>& sh, uint64_t& bar, uint32_t parity) {
+  const uint32_t b = tc::smem_u32(&bar);
+  uint64_t t0 = 0;
+  for (uint32_t i = 0; i < kKvPolls; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(b), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 63u) == 63u) {
+      if (*reinterpret_cast<volatile int*>(&sh.abort)) return false;
+      const uint64_t now = tc::globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > tc::kWaitLimitNs) break;
+    }
+  }
+  *reinterpret_cast<volatile int*>(&sh.abort) = 1;
+  return false;
+}
+
+// ---- producer --------------------------------------------------------------------------
+template <class C>
+__device__ void produce(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uint32_t smem, const CUtensorMap* kmap,
+                        const CUtensorMap* vmap) {
+  const int lane = threadIdx.x & 31;
+  const int page = 1 << a.page_log2, ppt = kKeys >> a.page_log2;
+  const uint32_t page_bytes = (uint32_t)page * C::kHD;
+  uint32_t bad = 0;
+  int64_t nk = 0, nv = 0;  // tiles of K and of V whose copies were issued
+  bool ok = true;
+  Walk w;
+  for (w.start(a, s, sh.share); ok && w.left > 0; w.next(a, s)) {
+    const int h = w.hh / s.nhb;
+    const int32_t* row = a.table + (int64_t)w.r * a.max_pages;
+    const int p_end = (w.g.hi + page - 1) >> a.page_log2, p_beg = w.g.lo >> a.page_log2;
+    int base = -1;       // first page of the 32 ids held, one per lane
+    int32_t ids = -1, ahead = -1;
+    for (int i = 0; i < w.take; ++i) {
+      const int p0 = (w.g.tile + w.off + i) * ppt;
+      if (base < 0 || p0 >= base + 32) {
+        const bool next = base >= 0;
+        base = p0;
+        ids = next ? ahead : (base + lane >= p_beg && base + lane < p_end ? row[base + lane] : -1);
+        ahead = base + 32 + lane < p_end ? row[base + 32 + lane] : -1;
+      }
+      const int32_t id = __shfl_sync(0xffffffffu, ids, (p0 - base + lane) & 31);
+      const int p = p0 + lane;
+      const bool in = lane < ppt && p >= p_beg && p < p_end && w.g.lo < w.g.hi;
+      const bool valid = in && id >= 0 && id < a.n_pages;
+      if (in && !valid) bad |= CSA2_DEV_BAD_INDEX;
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, valid)) * page_bytes;
+      const int st = (int)(nk % C::kStages);
+      const uint32_t parity = (uint32_t)(nk / C::kStages + 1) & 1u;
+      const int64_t head = (int64_t)id * a.Hk + h;
+      const int at = (int)(head << a.page_log2);
+      ok = __all_sync(0xffffffffu, kv_wait(sh, sh.kempty[st], parity));
+      if (!ok) break;
+      const uint32_t kb = tc::smem_u32(&sh.kfull[st]);
+      if (lane == 0) tc::mbar_arrive_expect_tx(kb, bytes);
+      __syncwarp();
+      if (valid) tma_rows(smem + C::kOffK + st * C::kTile + lane * page_bytes, kmap, at, kb);
+      ++nk;
+      ok = __all_sync(0xffffffffu, kv_wait(sh, sh.vempty[st], parity));
+      if (!ok) break;
+      const uint32_t vb = tc::smem_u32(&sh.vfull[st]);
+      if (lane == 0) tc::mbar_arrive_expect_tx(vb, bytes);
+      __syncwarp();
+      if (valid) {
+        tma_rows(smem + C::kOffV + st * C::kTile + lane * page_bytes, vmap, at, vb);
+        tc::cp_async4(tc::smem_u32(&sh.ks[st][lane]), a.k_scale + head);
+        tc::cp_async4(tc::smem_u32(&sh.vs[st][lane]), a.v_scale + head);
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(vb) : "memory");
+      } else {
+        if (lane < ppt) {  // no page: its rows are masked
+          sh.ks[st][lane] = 0.0f;
+          sh.vs[st][lane] = -1.0f;
+        }
+        tc::mbar_arrive(vb);
+      }
+      ++nv;
+    }
+  }
+  if (!ok) {  // given up: no copy may land after the CTA has gone
+    for (int64_t n = nk > C::kStages ? nk - C::kStages : 0; n < nk; ++n)
+      tc::mbar_wait(tc::smem_u32(&sh.kfull[n % C::kStages]), (uint32_t)(n / C::kStages) & 1u, kKvPolls);
+    for (int64_t n = nv > C::kStages ? nv - C::kStages : 0; n < nv; ++n)
+      tc::mbar_wait(tc::smem_u32(&sh.vfull[n % C::kStages]), (uint32_t)(n / C::kStages) & 1u, kKvPolls);
+  }
+  if (bad) flag(a.status, bad);
+}
+
+// ---- products (one thread) -------------------------------------------------------------
+template <class C>
+__device__ void multiply(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uint32_t smem, uint32_t tmem) {
+  constexpr uint32_t kIdS = idesc_e4m3(kKeys, C::NS, false, false);
+  constexpr uint32_t kIdO = idesc_e4m3(128, C::NP, true, true);
+  // K tile and queries: rows of HD bytes, K-major.  V tile: the same bytes read MN-major (with
+  // 64 channels the second half of the 128 M rows repeats the first: leading offset 0).  P:
+  // granules of 16 columns x 128 keys, 16 bytes per key, MN-major, no swizzle.
+  const uint64_t dk0 = tc::smem_desc(smem + C::kOffK, 16, 8 * C::kHD, C::kSwz);
+  const uint64_t dq = tc::smem_desc(smem + C::kOffQ, 16, 8 * C::kHD, C::kSwz);
+  const uint64_t dv0 = tc::smem_desc(smem + C::kOffV, 0, 8 * C::kHD, C::kSwz);
+  const uint64_t dp = tc::smem_desc(smem + C::kOffP, 128, 16 * kKeys, 0);
+  int64_t n = 0;
+  uint32_t piece = 0;
+  bool ok = true;
+  Walk w;
+  auto scores = [&](int64_t m) {  // S of tile m
+    const int st = (int)(m % C::kStages);
+    ok = kv_wait(sh, sh.kfull[st], (uint32_t)(m / C::kStages) & 1u) &&
+         kv_wait(sh, sh.sfree[m & 1], ((uint32_t)(m >> 1) & 1u) ^ 1u);
+    if (!ok) return;
+    tc::fence_after_sync();
+    const uint64_t dk = tc::desc_add(dk0, st * C::kTile);
+    const uint32_t d = tmem + C::kColS + (uint32_t)(m & 1) * C::NS;
+#pragma unroll
+    for (int k = 0; k < C::kHD / 32; ++k)
+      mma_e4m3(d, tc::desc_add(dk, 32 * k), tc::desc_add(dq, 32 * k), kIdS, k > 0);
+    tc::commit(tc::smem_u32(&sh.sfull[m & 1]));
+    tc::commit(tc::smem_u32(&sh.kempty[st]));
+  };
+  for (w.start(a, s, sh.share); ok && w.left > 0; w.next(a, s), ++piece) {
+    ok = kv_wait(sh, sh.qfull, piece & 1u);
+    if (!ok) break;
+    scores(n);
+    for (int i = 0; ok && i < w.take; ++i, ++n) {
+      if (i + 1 < w.take) scores(n + 1);
+      const int st = (int)(n % C::kStages);
+      ok = ok && kv_wait(sh, sh.vfull[st], (uint32_t)(n / C::kStages) & 1u) &&
+           kv_wait(sh, sh.pfull, (uint32_t)n & 1u);
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint64_t dv = tc::desc_add(dv0, st * C::kTile);
+#pragma unroll
+      for (int k = 0; k < kKeys / 32; ++k)
+        mma_e4m3(tmem + C::kColO, tc::desc_add(dv, 32 * k * C::kHD), tc::desc_add(dp, 32 * k * 16), kIdO,
+                 i > 0 || k > 0);
+      tc::commit(tc::smem_u32(&sh.vempty[st]));
+      tc::commit(tc::smem_u32(&sh.pvdone));
+    }
+  }
+  if (!ok) {  // given up: no product may run after the tensor memory is freed
+    tc::commit(tc::smem_u32(&sh.drain));
+    tc::mbar_wait(tc::smem_u32(&sh.drain), 0, kKvPolls);
+  }
+}
+
+// ---- softmax -----------------------------------------------------------------------------
+// Query rows of the piece as E4M3 digits (row d * NC + column of the Q operand), and what each
+// column needs later.
+template <class C, typename T>
+__device__ __forceinline__ void load_queries(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uint32_t smem,
+                                             const Walk& w) {
+  constexpr int kWarps = C::kSoft / 32, kPer = C::kHD / 32;  // elements per lane
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int h = w.hh / s.nhb, hb = w.hh % s.nhb;
+  const int nh = s.G - hb * s.HB < s.HB ? s.G - hb * s.HB : s.HB;  // heads in this block
+#pragma unroll 4
+  for (int c = warp; c < C::NC; c += kWarps) {
+    const int qi = c / s.HB, hd = c - qi * s.HB;
+    const int i = w.qb * s.QB + qi;
+    const bool live = qi < s.QB && i < w.x.n && hd < nh;
+    const int head = h * s.G + hb * s.HB + hd;
+    uint32_t raw[kPer / 2];
+#pragma unroll
+    for (int k = 0; k < kPer / 2; ++k) raw[k] = 0;
+    if (live) {
+      const uint8_t* p = a.q + (int64_t)(w.x.q0 + i) * a.q_stride + (int64_t)head * (C::kHD * 2) + lane * (kPer * 2);
+      if constexpr (kPer == 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        raw[0] = v.x;
+        raw[1] = v.y;
+      } else {
+        raw[0] = *reinterpret_cast<const uint32_t*>(p);
+      }
+    }
+    float x[kPer];
+    float amax = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kPer / 2; ++k) {
+      if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&raw[k]));
+        x[2 * k] = f.x;
+        x[2 * k + 1] = f.y;
+      } else {
+        x[2 * k] = bf16_lo(raw[k]);
+        x[2 * k + 1] = bf16_hi(raw[k]);
+      }
+      amax = fmaxf(amax, fmaxf(fabsf(x[2 * k]), fabsf(x[2 * k + 1])));
+    }
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+    int e = (int)(__float_as_uint(amax) >> 23) - 127;  // amax in [2^e, 2^(e+1))
+    e = e < -100 ? -100 : e;
+    const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) x[k] *= up;
+#pragma unroll
+    for (int d = 0; d < C::DQ; ++d) {
+      uint32_t word = 0;
+#pragma unroll
+      for (int k = 0; k < kPer / 2; ++k) {
+        const uint32_t b = e4m3x2_sat(x[2 * k], x[2 * k + 1]);
+        word |= b << (16 * k);
+        const uint32_t back = f16x2_of_e4m3x2(b);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+        x[2 * k] = (x[2 * k] - f.x) * 16.0f;
+        x[2 * k + 1] = (x[2 * k + 1] - f.y) * 16.0f;
+      }
+      const uint32_t at = smem + C::kOffQ + tc::swz(d * C::NC + c, lane * kPer, C::kHD);
+      if constexpr (kPer == 4) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(word) : "memory");
+      else asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)word) : "memory");
+    }
+    if (lane == 0) {
+      const float per = a.sm_scale * __uint_as_float((uint32_t)(127 + e - 7) << 23);
+      sh.qscale[c] = C::CAP ? per / a.softcap : per * kLog2e;
+      const int64_t pos = (int64_t)w.x.pos0 + i;
+      const int64_t hi = pos + 1, lo = a.window > 0 ? pos + 1 - a.window : 0;
+      sh.col_hi[c] = !live || hi < 0 ? 0 : (hi < w.x.cap ? (int)hi : w.x.cap);
+      sh.col_lo[c] = lo < 0 ? 0 : (lo < 0x7FFFFFFF ? (int)lo : 0x7FFFFFFF);
+      sh.col_row[c] = live ? (int64_t)(w.x.q0 + i) * a.Hq + head : -1;
+    }
+  }
+}
+
+template <class C, typename T>
+__device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uint8_t* smem_p, uint32_t tmem) {
+  constexpr int CW = C::CW;
+  const uint32_t smem = tc::smem_u32(smem_p);
+  const int tid = threadIdx.x, lane = tid & 31, wg = tid >> 7, wq = (tid >> 5) & 3, row = tid & 127;
+  const int bar = 1 + wg;
+  const int c0 = wg * CW;
+  const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
+  const float cap2 = C::CAP ? a.softcap * kLog2e : 0.0f;
+  int32_t* meta = a.meta + (int64_t)blockIdx.x * kMetaInts;
+  if (tid < 2) meta[tid] = 0;
+  bool bad = false;
+  int64_t n = 0;
+  Walk w;
+  for (w.start(a, s, sh.share); w.left > 0; w.next(a, s)) {
+    load_queries<C, T>(a, s, sh, smem, w);
+    tc::fence_async_smem();
+    asm volatile("bar.sync 3, %0;" ::"n"(C::kSoft) : "memory");  // columns known to every softmax thread
+    tc::mbar_arrive(tc::smem_u32(&sh.qfull));
+    float qs[CW], m[CW], l[CW];
+#pragma unroll
+    for (int c = 0; c < CW; ++c) {
+      qs[c] = sh.qscale[c0 + c];
+      m[c] = 0.0f;
+      l[c] = 0.0f;
+    }
+    uint32_t unseen = 0xffffffffu >> (32 - CW);  // columns that have seen no key yet
+    // keys that every live column sees: the block's first query ends soonest, its last starts latest
+    const int last_q = (w.qb + 1) * s.QB < w.x.n ? (w.qb + 1) * s.QB - 1 : w.x.n - 1;
+    const int64_t all_hi64 = (int64_t)w.x.pos0 + w.qb * s.QB + 1;
+    const int all_hi = all_hi64 < 0 ? 0 : (all_hi64 < w.x.cap ? (int)all_hi64 : w.x.cap);
+    const int64_t all_lo64 = a.window > 0 ? (int64_t)w.x.pos0 + last_q + 1 - a.window : 0;
+    for (int i = 0; i < w.take; ++i, ++n) {
+      const int st = (int)(n % C::kStages);
+      bad |= !kv_wait(sh, sh.sfull[n & 1], (uint32_t)(n >> 1) & 1u);
+      bad |= !kv_wait(sh, sh.vfull[st], (uint32_t)(n / C::kStages) & 1u);
+      tc::fence_after_sync();
+      float u[CW];
+      {
+        const uint32_t at = lanes + C::kColS + (uint32_t)(n & 1) * C::NS + c0;
+        uint32_t d[CW];
+        tmem_ld<CW>(at, d);
+#pragma unroll
+        for (int c = 0; c < CW; ++c) u[c] = __uint_as_float(d[c]);
+        tmem_ld<CW>(at + C::NC, d);
+#pragma unroll
+        for (int c = 0; c < CW; ++c) u[c] = fmaf(__uint_as_float(d[c]), 0.0625f, u[c]);
+        if constexpr (C::DQ == 3) {
+          tmem_ld<CW>(at + 2 * C::NC, d);
+#pragma unroll
+          for (int c = 0; c < CW; ++c) u[c] = fmaf(__uint_as_float(d[c]), 0.00390625f, u[c]);
+        }
+      }
+      tc::fence_before_sync();
+      tc::mbar_arrive(tc::smem_u32(&sh.sfree[n & 1]));
+      const int key0 = (w.g.tile + w.off + i) * kKeys, key = key0 + row;
+      const float ks = sh.ks[st][row >> a.page_log2];
+      float vs = sh.vs[st][row >> a.page_log2];
+      const bool there = vs >= 0.0f && key >= w.g.lo && key < w.g.hi;
+      vs = fmaxf(vs, 5.421010862427522e-20f);  // 2^-64
+      const float lv = __log2f(vs), per_v = __fdividef(1.0f, vs);
+      if constexpr (C::CAP) {
+        // cap * tanh(x), tanh(x) = 1 - 2 / (1 + e^2x): absolute error near 2^-23 of the cap
+#pragma unroll
+        for (int c = 0; c < CW; ++c) {
+          const float e2 = exp2_approx(fminf(u[c] * ks * qs[c] * (2.0f * kLog2e), 126.0f));
+          u[c] = fmaf(cap2, 1.0f - __fdividef(2.0f, 1.0f + e2), lv - m[c]);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < CW; ++c) u[c] = fmaf(u[c] * ks, qs[c], lv - m[c]);
+      }
+      if (!there) {
+#pragma unroll
+        for (int c = 0; c < CW; ++c) u[c] = -INFINITY;
+      } else if (key0 + kKeys > all_hi || key0 < all_lo64) {
+#pragma unroll
+        for (int c = 0; c < CW; ++c)
+          if (key >= sh.col_hi[c0 + c] || key < sh.col_lo[c0 + c]) u[c] = -INFINITY;
+      }
+      bool exceed = false;
+#pragma unroll
+      for (int c = 0; c < CW; ++c) exceed |= u[c] > kSlack;
+      if (unseen) {
+#pragma unroll
+        for (int c = 0; c < CW; ++c) exceed |= ((unseen >> c) & 1u) && u[c] > -INFINITY;
+      }
+      if (tc::named_sync_or(bar, 128, exceed || bad)) {
+        if (tc::named_sync_or(bar, 128, bad)) {
+          bad = true;
+          break;
+        }
+        float t[CW];
+#pragma unroll
+        for (int c = 0; c < CW; ++c) t[c] = u[c];
+        const float top = warp_columns<CW, true>(t, lane);
+        if (lane < CW) sh.red[wg][wq][lane] = top;
+        asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
+        if (i > 0) bad |= !kv_wait(sh, sh.pvdone, (uint32_t)(n - 1) & 1u);
+        tc::fence_after_sync();
+        float f[CW];
+#pragma unroll
+        for (int c = 0; c < CW; ++c) {
+          const float mx = fmaxf(fmaxf(sh.red[wg][0][c], sh.red[wg][1][c]), fmaxf(sh.red[wg][2][c], sh.red[wg][3][c]));
+          const bool fresh = (unseen >> c) & 1u;
+          const float up = mx == -INFINITY ? 0.0f : (fresh ? mx : (mx > kSlack ? mx : 0.0f));
+          if (fresh && mx != -INFINITY) unseen &= ~(1u << c);
+          f[c] = fresh ? 1.0f : exp2_approx(-up);
+          m[c] += up;
+          l[c] *= f[c];
+          u[c] -= up;
+        }
+        if (i > 0) {  // the accumulated output under the new maxima
+#pragma unroll
+          for (int d = 0; d < 3; ++d) {
+            uint32_t o[CW];
+            tmem_ld<CW>(lanes + C::kColO + d * C::NC + c0, o);
+#pragma unroll
+            for (int c = 0; c < CW; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f[c]);
+            tmem_st<CW>(lanes + C::kColO + d * C::NC + c0, o);
+          }
+          tc::tmem_wait_st();
+        }
+        asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");  // red may be written again
+      } else if (i > 0) {
+        bad |= !kv_wait(sh, sh.pvdone, (uint32_t)(n - 1) & 1u);  // P may be written again
+      }
+      uint32_t dig[3][CW / 4];
+#pragma unroll
+      for (int c = 0; c < CW; c += 4) {
+        uint32_t b[3][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float p0 = exp2_approx(u[c + 2 * k] + kLift), p1 = exp2_approx(u[c + 2 * k + 1] + kLift);
+          l[c + 2 * k] = fmaf(p0, per_v, l[c + 2 * k]);
+          l[c + 2 * k + 1] = fmaf(p1, per_v, l[c + 2 * k + 1]);
+          const __half2 ph = __floats2half2_rn(p0, p1);
+          uint32_t p = *reinterpret_cast<const uint32_t*>(&ph);
+          b[0][k] = e4m3x2_of_f16x2(p);
+          p = rest16(p, f16x2_of_e4m3x2(b[0][k]));
+          b[1][k] = e4m3x2_of_f16x2(p);
+          p = rest16(p, f16x2_of_e4m3x2(b[1][k]));
+          b[2][k] = e4m3x2_of_f16x2(p);
+        }
+#pragma unroll
+        for (int d = 0; d < 3; ++d) dig[d][c / 4] = b[d][0] | (b[d][1] << 16);
+      }
+#pragma unroll
+      for (int d = 0; d < 3; ++d) {
+        const int col = d * C::NC + c0;
+        const uint32_t at = smem + C::kOffP + (col / 16) * (16 * kKeys) + row * 16 + col % 16;
+        if constexpr (CW == 8) {
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(dig[d][0]), "r"(dig[d][1]) : "memory");
+        } else {
+#pragma unroll
+          for (int k = 0; k < CW / 16; ++k)
+            tc::st_shared_v4(at + k * (16 * kKeys),
+                             make_uint4(dig[d][4 * k], dig[d][4 * k + 1], dig[d][4 * k + 2], dig[d][4 * k + 3]));
+        }
+      }
+      if (!there && wg == 0) {  // whatever lies there (NaN included) times a zero probability
+#pragma unroll
+        for (int k = 0; k < C::kHD / 16; ++k)
+          tc::st_shared_v4(smem + C::kOffV + st * C::kTile + row * C::kHD + k * 16, make_uint4(0u, 0u, 0u, 0u));
+      }
+      tc::fence_async_smem();
+      tc::fence_before_sync();
+      tc::mbar_arrive(tc::smem_u32(&sh.pfull));
+    }
+    if (!bad) bad = !kv_wait(sh, sh.pvdone, (uint32_t)(n - 1) & 1u);
+    if (tc::named_sync_or(3, C::kSoft, bad)) break;
+    tc::fence_after_sync();
+    // sums over the keys: the warp's rows, then the four warps
+    const float sum = warp_columns<CW, false>(l, lane);
+    if (lane < CW) sh.red[wg][wq][lane] = sum;
+    asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
+    const bool whole = w.first && w.last;
+    const int slot = w.first ? 1 : 0;
+    float* part = a.part + ((int64_t)blockIdx.x * 2 + slot) * (C::NC * (C::kHD + 2));
+    if (row < CW) {
+      const float tot = (sh.red[wg][0][row] + sh.red[wg][1][row]) + (sh.red[wg][2][row] + sh.red[wg][3][row]);
+      float mm = 0.0f;
+#pragma unroll
+      for (int c = 0; c < CW; ++c) mm = row == c ? m[c] : mm;
+      const int64_t to = sh.col_row[c0 + row];
+      if (whole) {
+        sh.linv[c0 + row] = tot > 0.0f ? __fdiv_rn(1.0f, tot) : 0.0f;
+        if (a.lse && to >= 0) a.lse[to] = tot > 0.0f ? (mm + log2f(tot) - kLift) * kLn2 : -INFINITY;
+      } else {
+        part[C::NC * C::kHD + 2 * (c0 + row)] = mm;
+        part[C::NC * C::kHD + 2 * (c0 + row) + 1] = tot;
+      }
+    }
+    asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
+    {
+      float o[CW];
+      uint32_t d[CW];
+      tmem_ld<CW>(lanes + C::kColO + c0, d);
+#pragma unroll
+      for (int c = 0; c < CW; ++c) o[c] = __uint_as_float(d[c]);
+      tmem_ld<CW>(lanes + C::kColO + C::NC + c0, d);
+#pragma unroll
+      for (int c = 0; c < CW; ++c) o[c] = fmaf(__uint_as_float(d[c]), 0.0625f, o[c]);
+      tmem_ld<CW>(lanes + C::kColO + 2 * C::NC + c0, d);
+#pragma unroll
+      for (int c = 0; c < CW; ++c) o[c] = fmaf(__uint_as_float(d[c]), 0.00390625f, o[c]);
+      if (row < C::kHD) {
+        if (whole) {
+          T* out = reinterpret_cast<T*>(a.out);
+#pragma unroll
+          for (int c = 0; c < CW; ++c) {
+            const int64_t to = sh.col_row[c0 + c];
+            if (to >= 0) out[to * C::kHD + row] = from_float<T>(o[c] * sh.linv[c0 + c]);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < CW; ++c) part[(c0 + c) * C::kHD + row] = o[c];
+        }
+      }
+    }
+    tc::fence_before_sync();
+    if (!whole && tid == 0) {
+      if (w.first) {
+        meta[1] = 1;
+        meta[2] = w.r;
+        meta[3] = w.hh;
+        meta[4] = w.qb;
+      } else {
+        meta[0] = w.last ? 2 : 1;
+      }
+    }
+    // the next piece's queries may replace these: every product of this one has completed, and
+    // every softmax thread has read its columns
+    asm volatile("bar.sync 3, %0;" ::"n"(C::kSoft) : "memory");
+  }
+}
+
+template <class C, typename T>
+__global__ void __launch_bounds__(C::kThreads) kv8_attn_kernel(const __grid_constant__ CUtensorMap kmap,
+                                                                const __grid_constant__ CUtensorMap vmap,
+                                                                const KvAttnArgs a) {
+  extern __shared__ uint8_t raw[];
+  __shared__ KvShared<C> sh;
+  uint8_t* smem = tc::align_smem_1024(raw);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      tc::mbar_init(tc::smem_u32(&sh.kfull[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh.vfull[i]), 33);
+      tc::mbar_init(tc::smem_u32(&sh.kempty[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh.vempty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(tc::smem_u32(&sh.sfull[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh.sfree[i]), C::kSoft);
+    }
+    tc::mbar_init(tc::smem_u32(&sh.qfull), C::kSoft);
+    tc::mbar_init(tc::smem_u32(&sh.pfull), C::kSoft);
+    tc::mbar_init(tc::smem_u32(&sh.pvdone), 1);
+    tc::mbar_init(tc::smem_u32(&sh.drain), 1);
+    sh.abort = 0;
+  }
+  // Tensor memory is taken only when the predecessor has returned its own, and the successor
+  // may start only when this CTA has taken its: kernels that wait for one another through
+  // the launch order never also wait for one another's tensor memory.
+  chain_wait();
+  if (warp == 0) tc::tmem_alloc(tc::smem_u32(&sh.tmem), C::kCols);
+  const Shape s = shape_of<C::NC>(a);
+  uint32_t bad = 0;
+  find_share<C::kThreads>(a, s, sh.sums, &sh.share, &bad);
+  if (bad && blockIdx.x == 0) flag(a.status, bad);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  chain_launch_dependents();
+  const uint32_t tmem = sh.tmem;
+  if (warp < C::kSoft / 32) {
+    soften<C, T>(a, s, sh, smem, tmem);
+  } else if (warp == C::kSoft / 32) {
+    produce<C>(a, s, sh, tc::smem_u32(smem), &kmap, &vmap);
+  } else if ((tid & 31) == 0) {
+    multiply<C>(a, s, sh, tc::smem_u32(smem), tmem);
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 0) tc::tmem_dealloc(tmem, C::kCols);
+  if (tid == 0 && sh.abort) flag(a.status, CSA2_DEV_TIMEOUT);
+}
+
+// Joins the pieces of the item that CTA blockIdx.x starts and does not end: with M the largest
+// of the pieces' maxima, out = sum 2^(m - M) O / sum 2^(m - M) l.  blockIdx.y: 8 columns; a
+// thread one channel of them.
+template <class C, typename T>
+__global__ void __launch_bounds__(C::kHD) kv8_merge_kernel(const KvAttnArgs a, int ctas) {
+  chain_enter();
+  const int cta = blockIdx.x, c0 = blockIdx.y * 8, d = threadIdx.x;
+  const int32_t* meta = a.meta + (int64_t)cta * kMetaInts;
+  if (meta[1] == 0) return;
+  const Shape s = shape_of<C::NC>(a);
+  const int r = meta[2], hh = meta[3], qb = meta[4];
+  uint32_t bad = 0;
+  const Request x = request_of(a, s, r, &bad);
+  constexpr int kPart = C::NC * (C::kHD + 2);
+  float M[8], l[8], o[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    M[j] = -INFINITY;
+    l[j] = 0.0f;
+    o[j] = 0.0f;
+  }
+  for (int k = cta; k < ctas; ++k) {
+    const bool mine = k == cta;
+    const int state = mine ? 1 : a.meta[(int64_t)k * kMetaInts];
+    if (state == 0) continue;  // a CTA without work
+    const float* p = a.part + ((int64_t)k * 2 + (mine ? 1 : 0)) * kPart;
+    float po[8];
+    float2 ml[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      po[j] = p[(c0 + j) * C::kHD + d];
+      ml[j] = *reinterpret_cast<const float2*>(p + C::NC * C::kHD + 2 * (c0 + j));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (ml[j].y > 0.0f) {  // a piece that saw no key has no maximum
+        const float top = fmaxf(M[j], ml[j].x), fa = exp2f(M[j] - top), fb = exp2f(ml[j].x - top);
+        l[j] = l[j] * fa + ml[j].y * fb;
+        o[j] = o[j] * fa + po[j] * fb;
+        M[j] = top;
+      }
+    }
+    if (state == 2) break;
+  }
+  const int hb = hh % s.nhb;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int c = c0 + j, qi = c / s.HB, hd = c - qi * s.HB, i = qb * s.QB + qi;
+    if (qi >= s.QB || i >= x.n || hd >= s.G - hb * s.HB) continue;
+    const int64_t to = (int64_t)(x.q0 + i) * a.Hq + hh / s.nhb * s.G + hb * s.HB + hd;
+    reinterpret_cast<T*>(a.out)[to * C::kHD + d] = from_float<T>(l[j] > 0.0f ? o[j] / l[j] : 0.0f);
+    if (a.lse && d == 0) a.lse[to] = l[j] > 0.0f ? (M[j] + log2f(l[j]) - kLift) * kLn2 : -INFINITY;
+  }
+}
+
+// ---- host --------------------------------------------------------------------------------
+// Columns per tile: the smallest of 8, 16, 32, 64 that holds a request's queries times the
+// heads of a group, so decode pays for no empty columns and long chunks share each tile's
+// keys most; fp16 queries stop at 32 (three digits of 64 columns exceed the tensor memory).
+static int columns_of(int Hq, int Hk, int max_q, int f16) {
+  const int64_t want = (int64_t)(Hq / Hk) * (max_q < 1 ? 1 : max_q);
+  const int most = f16 ? 32 : 64;
+  int nc = 8;
+  while (nc < most && nc < want) nc *= 2;
+  return nc;
+}
+static int ctas_of(int nc, int num_sms) { return num_sms * (nc <= 16 ? 2 : 1); }
+
+size_t kv8_attn_workspace_bytes(int Hq, int Hk, int hd, int max_q, int f16, int num_sms) {
+  const int nc = columns_of(Hq, Hk, max_q, f16), ctas = ctas_of(nc, num_sms);
+  return (size_t)ctas * 2 * nc * (hd + 2) * sizeof(float) + (size_t)ctas * kMetaInts * sizeof(int32_t);
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// The cache as rows of hd bytes; a box is one head's rows of one page.
+static bool encode_rows(CUtensorMap* m, const uint8_t* cache, int64_t rows, int hd, int page) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)hd, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)hd};
+  const cuuint32_t box[2] = {(cuuint32_t)hd, (cuuint32_t)page}, one[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(cache), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class C, typename T>
+static cudaError_t launch_kv8_t(const CUtensorMap& km, const CUtensorMap& vm, KvAttnArgs a, void* ws, int num_sms,
+                                cudaStream_t stream) {
+  const int ctas = num_sms * C::kCtas;
+  a.part = static_cast<float*>(ws);
+  a.meta = reinterpret_cast<int32_t*>(a.part + (size_t)ctas * 2 * C::NC * (C::kHD + 2));
+  cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<C, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_chained(kv8_attn_kernel<C, T>, dim3(ctas), dim3(C::kThreads), C::kSmem, stream, 0, km, vm, a);
+  if (e != cudaSuccess) return e;
+  e = launch_chained(kv8_merge_kernel<C, T>, dim3(ctas, C::NC / 8), dim3(C::kHD), 0, stream, 0, a, ctas);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int HD, int DQ, bool CAP, typename T>
+static cudaError_t launch_kv8_nc(int nc, const CUtensorMap& km, const CUtensorMap& vm, const KvAttnArgs& a, void* ws,
+                                 int num_sms, cudaStream_t stream) {
+  if (nc == 8) return launch_kv8_t<KvCfg<HD, 8, DQ, CAP>, T>(km, vm, a, ws, num_sms, stream);
+  if (nc == 16) return launch_kv8_t<KvCfg<HD, 16, DQ, CAP>, T>(km, vm, a, ws, num_sms, stream);
+  if (nc == 32) return launch_kv8_t<KvCfg<HD, 32, DQ, CAP>, T>(km, vm, a, ws, num_sms, stream);
+  if constexpr (DQ == 2) return launch_kv8_t<KvCfg<HD, 64, DQ, CAP>, T>(km, vm, a, ws, num_sms, stream);
+  return cudaErrorInvalidValue;
+}
+
+template <int HD, bool CAP>
+static cudaError_t launch_kv8_type(int f16, int nc, const CUtensorMap& km, const CUtensorMap& vm, const KvAttnArgs& a,
+                                   void* ws, int num_sms, cudaStream_t stream) {
+  return f16 ? launch_kv8_nc<HD, 3, CAP, __half>(nc, km, vm, a, ws, num_sms, stream)
+             : launch_kv8_nc<HD, 2, CAP, __nv_bfloat16>(nc, km, vm, a, ws, num_sms, stream);
+}
+
+cudaError_t launch_kv8_attn(const void* q, int64_t q_stride, int f16, int64_t T, int Hq, int Hk, int hd,
+                            const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                            int64_t n_pages, int page, const int32_t* table, int max_pages, const int32_t* q_start,
+                            const int32_t* seq_len, int R, int max_q, float sm_scale, int window, float softcap,
+                            void* out, float* lse, void* ws, uint32_t* status, cudaStream_t stream, int num_sms) {
+  KvAttnArgs a = {};
+  a.q = static_cast<const uint8_t*>(q);
+  a.q_stride = q_stride * 2;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.table = table;
+  a.q_start = q_start;
+  a.seq_len = seq_len;
+  a.R = R;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.max_pages = max_pages;
+  a.page_log2 = log2_of(page);
+  a.n_pages = n_pages;
+  a.T = T;
+  a.sm_scale = sm_scale;
+  a.window = window;
+  a.softcap = softcap;
+  a.out = static_cast<uint8_t*>(out);
+  a.lse = lse;
+  a.status = status;
+  CUtensorMap km, vm;
+  const int64_t rows = n_pages * Hk * page;
+  if (!encode_rows(&km, k_cache, rows, hd, page) || !encode_rows(&vm, v_cache, rows, hd, page))
+    return cudaErrorInvalidValue;
+  const int nc = columns_of(Hq, Hk, max_q, f16);
+  if (hd == 64)
+    return softcap > 0.0f ? launch_kv8_type<64, true>(f16, nc, km, vm, a, ws, num_sms, stream)
+                          : launch_kv8_type<64, false>(f16, nc, km, vm, a, ws, num_sms, stream);
+  return softcap > 0.0f ? launch_kv8_type<128, true>(f16, nc, km, vm, a, ws, num_sms, stream)
+                        : launch_kv8_type<128, false>(f16, nc, km, vm, a, ws, num_sms, stream);
+}
+
+}  // namespace csa2
