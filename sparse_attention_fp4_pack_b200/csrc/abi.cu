@@ -49,7 +49,7 @@ cudaError_t launch_kv8_append(const void* k, const void* v, int64_t k_stride, in
                               int Hk, int hd, const int64_t* slot, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,
                               float* v_scale, int64_t n_pages, int page, uint32_t* status, cudaStream_t stream,
                               int num_sms);
-size_t kv8_attn_workspace_bytes(int Hq, int Hk, int hd, int max_q, int f16, int num_sms);
+size_t kv8_attn_workspace_bytes(int Hq, int Hk, int hd, int max_q, int num_sms);
 cudaError_t launch_kv8_attn(const void* q, int64_t q_stride, int f16, int64_t T, int Hq, int Hk, int hd,
                             const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
                             int64_t n_pages, int page, const int32_t* table, int max_pages, const int32_t* q_start,
@@ -477,7 +477,7 @@ csa2_status csa2_kv8_append(const void* k, const void* v, int64_t k_stride, int6
 
 size_t csa2_kv8_attn_workspace_size(int Hq, int Hk, int hd, int max_q, int dtype) {
   if (Hk < 1 || Hq < Hk || Hq % Hk || (hd != 64 && hd != 128) || (dtype != CSA2_BF16 && dtype != CSA2_F16)) return 0;
-  return round256(csa2::kv8_attn_workspace_bytes(Hq, Hk, hd, max_q, dtype == CSA2_F16, current_sm_count()));
+  return round256(csa2::kv8_attn_workspace_bytes(Hq, Hk, hd, max_q < 1 ? 1 : max_q, current_sm_count()));
 }
 
 csa2_status csa2_kv8_attn(const void* q, int64_t q_stride, int dtype, int64_t T, int Hq, int Hk, int hd,

@@ -357,28 +357,6 @@ __device__ __forceinline__ float block_scale(float amax) {
   return __uint_as_float((uint32_t)(e < 63 ? 63 : e) << 23);
 }
 
-template <typename T>
-__device__ __forceinline__ void unpack8(uint4 w, float (&x)[8]);
-template <>
-__device__ __forceinline__ void unpack8<__nv_bfloat16>(uint4 w, float (&x)[8]) {
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_lo(v[i]);
-    x[2 * i + 1] = bf16_hi(v[i]);
-  }
-}
-template <>
-__device__ __forceinline__ void unpack8<__half>(uint4 w, float (&x)[8]) {
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-}
-
 // 8 values over the scale, encoded.  A power-of-two scale (every scale this call chooses)
 // divides exactly by its reciprocal; a page's earlier scale may be any fp32.
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float s, float inv, bool pow2) {

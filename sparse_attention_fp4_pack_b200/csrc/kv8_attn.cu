@@ -31,46 +31,16 @@
 
 #include "csa2_device.cuh"
 #include "kv8.cuh"
+#include "kv8_list.cuh"
 #include "tc.cuh"
 
 namespace csa2 {
 
-constexpr int kKeys = 128;             // keys per tile = UMMA M
-constexpr int kMaxTilePages = 8;       // pages of 16 rows
+constexpr int kMaxColumns = 32;
 constexpr float kLift = 6.0f;          // probabilities are 2^(t - max + 6), at most 2^8
-constexpr float kSlack = 2.0f;         // the running maximum is raised when exceeded by more (base 2)
-constexpr uint32_t kKvPolls = 1u << 22;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 __host__ __device__ constexpr int round16(int n) { return (n + 15) / 16 * 16; }
 constexpr uint32_t pow2_cols(int n) { return n <= 32 ? 32u : n <= 64 ? 64u : n <= 128 ? 128u : n <= 256 ? 256u : 512u; }
-
-struct KvAttnArgs {
-  const uint8_t* q;
-  int64_t q_stride;  // bytes from token to token
-  const float* k_scale;
-  const float* v_scale;
-  const int32_t* table;
-  const int32_t* q_start;
-  const int32_t* seq_len;
-  int R, Hq, Hk, max_pages, page_log2;
-  int64_t n_pages;
-  int64_t T;
-  float sm_scale;
-  int window;
-  float softcap;
-  uint8_t* out;
-  float* lse;
-  float* part;    // [CTA][2][NC][hd + 2]
-  int32_t* meta;  // [CTA][8]
-  uint32_t* status;
-};
-
-// Partial results of CTA c: slot 0 the piece that continues an item, slot 1 the one that
-// starts an item and does not end it.  meta: [0] slot 0 (0 none, 1 goes on, 2 ends the item),
-// [1] slot 1 used, [2..5] its request, head, head block, query block.
-constexpr int kMetaInts = 8;
 
 template <int HD, int NC_, int DQ_, bool CAP_>
 struct KvCfg {
@@ -108,18 +78,6 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uin
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
 }
-__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          dst),
-      "l"(map), "r"(0), "r"(row), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
   if constexpr (N == 8) tc::tmem_ld8(addr, r);
@@ -132,12 +90,6 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[N]) {
   else if constexpr (N == 16) tc::tmem_st16_nowait(addr, r);
   else tc::tmem_st32_nowait(addr, r);
 }
-template <typename T>
-__device__ __forceinline__ T from_float(float x);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-template <>
-__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
 // N values per lane -> lane i holds value i mod N reduced over the warp (N - 1 exchanges, then
 // the remaining whole-warp ones).
 template <int N, bool kMax>
@@ -169,248 +121,10 @@ __device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
   return r;
 }
-__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t b) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)b));
-  return r;
-}
 __device__ __forceinline__ uint32_t rest16(uint32_t p, uint32_t d) {  // (p - d) * 16, exact
   const __half2 r = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&p), *reinterpret_cast<__half2*>(&d)),
                             __floats2half2_rn(16.0f, 16.0f));
   return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// ---- the list of key tiles -------------------------------------------------------------
-struct Request {
-  int q0, n;     // first query row, queries
-  int pos0;      // position of the first query
-  int cap;       // keys: min(seq_len, what the table holds)
-  int nqb;       // query blocks
-};
-struct Shape {   // how a request's columns are cut
-  int G, QB, HB, nhb;
-};
-template <int NC>
-__device__ __forceinline__ Shape shape_of(const KvAttnArgs& a) {
-  Shape s;
-  s.G = a.Hq / a.Hk;
-  s.HB = s.G < NC ? s.G : NC;
-  s.QB = s.G < NC ? NC / s.G : 1;
-  s.nhb = (s.G + NC - 1) / NC;
-  return s;
-}
-__device__ __forceinline__ Request request_of(const KvAttnArgs& a, const Shape& s, int r, uint32_t* bad) {
-  Request x;
-  const int64_t b = a.q_start[r], e = a.q_start[r + 1];
-  int len = a.seq_len[r];
-  const int64_t q0 = b < 0 ? 0 : (b < a.T ? b : a.T), q1 = e < q0 ? q0 : (e < a.T ? e : a.T);
-  if (q0 != b || q1 != e || len < 0) *bad |= CSA2_DEV_BAD_COUNT;
-  if (len < 0) len = 0;
-  x.q0 = (int)q0;
-  x.n = (int)(q1 - q0);
-  if (x.n > len) *bad |= CSA2_DEV_BAD_COUNT;
-  x.pos0 = len - x.n;
-  const int64_t held = (int64_t)a.max_pages << a.page_log2;
-  if (len > held) *bad |= CSA2_DEV_BAD_COUNT;
-  x.cap = len < held ? len : (int)held;
-  x.nqb = (x.n + s.QB - 1) / s.QB;
-  return x;
-}
-// Keys [lo, hi) that any query of block qb sees, and its first tile and number of tiles (at
-// least one: a block that sees nothing still writes its rows).
-struct Range {
-  int lo, hi, tile, tiles;
-};
-__device__ __forceinline__ Range range_of(const KvAttnArgs& a, const Shape& s, const Request& x, int qb) {
-  Range g;
-  const int i0 = qb * s.QB, i1 = i0 + s.QB < x.n ? i0 + s.QB : x.n;
-  const int64_t hi = (int64_t)x.pos0 + i1;
-  g.hi = hi < 0 ? 0 : (hi < x.cap ? (int)hi : x.cap);
-  const int64_t lo = a.window > 0 ? (int64_t)x.pos0 + i0 + 1 - a.window : 0;
-  g.lo = lo < 0 ? 0 : (lo < g.hi ? (int)lo : g.hi);
-  g.tile = g.lo / kKeys;
-  const int end = (g.hi + kKeys - 1) / kKeys;
-  g.tiles = end > g.tile ? end - g.tile : 1;
-  return g;
-}
-// Tiles of one (request, key head, head block).
-__device__ __forceinline__ int64_t row_tiles(const KvAttnArgs& a, const Shape& s, const Request& x, int first, int step) {
-  int64_t n = 0;
-  for (int qb = first; qb < x.nqb; qb += step) n += range_of(a, s, x, qb).tiles;
-  return n;
-}
-__device__ __forceinline__ int64_t warp_sum(int64_t v) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-// row_tiles of request r for each lane (r < R where live), long requests by the whole warp.
-__device__ __forceinline__ int64_t lane_row_tiles(const KvAttnArgs& a, const Shape& s, int r, bool live, int lane,
-                                                  uint32_t* bad) {
-  Request x = {};
-  if (live) x = request_of(a, s, r, bad);
-  const bool big = x.nqb > 8;
-  int64_t n = big ? 0 : row_tiles(a, s, x, 0, 1);
-  unsigned todo = __ballot_sync(0xffffffffu, big);
-  while (todo) {
-    const int src = __ffs(todo) - 1;
-    todo &= todo - 1;
-    Request y;
-    y.q0 = __shfl_sync(0xffffffffu, x.q0, src);
-    y.n = __shfl_sync(0xffffffffu, x.n, src);
-    y.pos0 = __shfl_sync(0xffffffffu, x.pos0, src);
-    y.cap = __shfl_sync(0xffffffffu, x.cap, src);
-    y.nqb = __shfl_sync(0xffffffffu, x.nqb, src);
-    const int64_t m = warp_sum(row_tiles(a, s, y, lane, 32));
-    if (lane == src) n = m;
-  }
-  return n;
-}
-
-// This CTA's share of the list: its length, and where it begins.
-struct Share {
-  int64_t left;
-  int r, hh, qb, off;  // request, key head * nhb + head block, query block, tile inside the item
-};
-
-// A walk over a share's pieces; every role keeps its own.
-struct Walk {
-  int64_t left;
-  int r, hh, qb, off;
-  Request x;
-  Range g;
-  int take;        // tiles of this piece
-  bool first, last;
-  __device__ __forceinline__ void open(const KvAttnArgs& a, const Shape& s) {
-    g = range_of(a, s, x, qb);
-    const int rest = g.tiles - off;
-    take = left < rest ? (int)left : rest;
-    first = off == 0;
-    last = off + take == g.tiles;
-  }
-  __device__ __forceinline__ void start(const KvAttnArgs& a, const Shape& s, const Share& w) {
-    left = w.left;
-    r = w.r;
-    hh = w.hh;
-    qb = w.qb;
-    off = w.off;
-    if (left <= 0) return;
-    uint32_t bad = 0;
-    x = request_of(a, s, r, &bad);
-    open(a, s);
-  }
-  __device__ __forceinline__ void next(const KvAttnArgs& a, const Shape& s) {
-    left -= take;
-    off = 0;
-    if (left <= 0) return;
-    if (++qb < x.nqb) {
-      open(a, s);
-      return;
-    }
-    qb = 0;
-    if (++hh < a.Hk * s.nhb) {
-      open(a, s);
-      return;
-    }
-    hh = 0;
-    uint32_t bad = 0;
-    do {
-      if (++r >= a.R) {  // cannot happen while left > 0
-        left = 0;
-        return;
-      }
-      x = request_of(a, s, r, &bad);
-    } while (x.n == 0);
-    open(a, s);
-  }
-};
-
-// Computed by the whole CTA (kThreads threads); `sums` holds a value per thread.
-template <int kThreads>
-__device__ void find_share(const KvAttnArgs& a, const Shape& s, int64_t* sums, Share* out, uint32_t* bad) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int per = (a.R + kThreads - 1) / kThreads;  // requests per thread, consecutive
-  const int heads = a.Hk * s.nhb;
-  int64_t mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int r = tid * per + i;
-    mine += lane_row_tiles(a, s, r, r < a.R, lane, bad);
-  }
-  sums[tid] = mine * heads;
-  __syncthreads();
-  if (tid < 32) {
-    constexpr int kEach = kThreads / 32;
-    int64_t part = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) part += sums[lane * kEach + i];
-    int64_t upto = part;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += y;
-    }
-    const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
-    const int64_t c = blockIdx.x, C = gridDim.x;
-    const int64_t t0 = total / C * c + total % C * c / C, t1 = total / C * (c + 1) + total % C * (c + 1) / C;
-    Share w = {t1 - t0, 0, 0, 0, 0};
-    if (w.left > 0) {
-      // the thread whose requests hold tile t0 ...
-      const unsigned m = __ballot_sync(0xffffffffu, upto > t0);
-      const int l0 = __ffs(m) - 1;
-      int64_t before = __shfl_sync(0xffffffffu, upto - part, l0);
-      int th = l0 * kEach;
-      while (before + sums[th] <= t0) before += sums[th++];
-      // ... the request (32 at a time) ...
-      int64_t rest = t0 - before;
-      int r = th * per;
-      Request x;
-      int64_t row;
-      for (;;) {
-        const int64_t n = lane_row_tiles(a, s, r + lane, r + lane < a.R, lane, bad) * heads;
-        int64_t in = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, in, o);
-          if (lane >= o) in += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, in > rest);
-        if (hit) {
-          const int l = __ffs(hit) - 1;
-          rest -= __shfl_sync(0xffffffffu, in - n, l);
-          row = __shfl_sync(0xffffffffu, n, l) / heads;
-          r += l;
-          break;
-        }
-        rest -= __shfl_sync(0xffffffffu, in, 31);
-        r += 32;
-      }
-      x = request_of(a, s, r, bad);
-      w.r = r;
-      w.hh = (int)(rest / row);
-      rest -= (int64_t)w.hh * row;
-      // ... and the query block
-      for (int qb0 = 0;; qb0 += 32) {
-        const int n = qb0 + lane < x.nqb ? range_of(a, s, x, qb0 + lane).tiles : 0;
-        int64_t in = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, in, o);
-          if (lane >= o) in += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, in > rest);
-        if (hit) {
-          const int l = __ffs(hit) - 1;
-          w.qb = qb0 + l;
-          w.off = (int)(rest - __shfl_sync(0xffffffffu, in - n, l));
-          break;
-        }
-        rest -= __shfl_sync(0xffffffffu, in, 31);
-        if (qb0 + 32 >= x.nqb) break;  // cannot happen
-      }
-    }
-    if (lane == 0) *out = w;
-  }
-  __syncthreads();
 }
 
 // ---- shared state of a CTA -----------------------------------------------------------------
@@ -429,32 +143,6 @@ struct KvShared {
   float red[C::kGroups][4][C::CW];
   float linv[C::NC];
 };
-
-// Bounded wait that also ends when another role has given up.
-template <class C>
-__device__ __forceinline__ bool kv_wait(KvShared<C>& sh, uint64_t& bar, uint32_t parity) {
-  const uint32_t b = tc::smem_u32(&bar);
-  uint64_t t0 = 0;
-  for (uint32_t i = 0; i < kKvPolls; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(b), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((i & 63u) == 63u) {
-      if (*reinterpret_cast<volatile int*>(&sh.abort)) return false;
-      const uint64_t now = tc::globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      else if (now - t0 > tc::kWaitLimitNs) break;
-    }
-  }
-  *reinterpret_cast<volatile int*>(&sh.abort) = 1;
-  return false;
-}
 
 // ---- producer --------------------------------------------------------------------------
 template <class C>
@@ -491,14 +179,14 @@ __device__ void produce(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, ui
       const uint32_t parity = (uint32_t)(nk / C::kStages + 1) & 1u;
       const int64_t head = (int64_t)id * a.Hk + h;
       const int at = (int)(head << a.page_log2);
-      ok = __all_sync(0xffffffffu, kv_wait(sh, sh.kempty[st], parity));
+      ok = __all_sync(0xffffffffu, kv_wait(&sh.abort, sh.kempty[st], parity));
       if (!ok) break;
       const uint32_t kb = tc::smem_u32(&sh.kfull[st]);
       if (lane == 0) tc::mbar_arrive_expect_tx(kb, bytes);
       __syncwarp();
       if (valid) tma_rows(smem + C::kOffK + st * C::kTile + lane * page_bytes, kmap, at, kb);
       ++nk;
-      ok = __all_sync(0xffffffffu, kv_wait(sh, sh.vempty[st], parity));
+      ok = __all_sync(0xffffffffu, kv_wait(&sh.abort, sh.vempty[st], parity));
       if (!ok) break;
       const uint32_t vb = tc::smem_u32(&sh.vfull[st]);
       if (lane == 0) tc::mbar_arrive_expect_tx(vb, bytes);
@@ -545,8 +233,8 @@ __device__ void multiply(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, u
   Walk w;
   auto scores = [&](int64_t m) {  // S of tile m
     const int st = (int)(m % C::kStages);
-    ok = kv_wait(sh, sh.kfull[st], (uint32_t)(m / C::kStages) & 1u) &&
-         kv_wait(sh, sh.sfree[m & 1], ((uint32_t)(m >> 1) & 1u) ^ 1u);
+    ok = kv_wait(&sh.abort, sh.kfull[st], (uint32_t)(m / C::kStages) & 1u) &&
+         kv_wait(&sh.abort, sh.sfree[m & 1], ((uint32_t)(m >> 1) & 1u) ^ 1u);
     if (!ok) return;
     tc::fence_after_sync();
     const uint64_t dk = tc::desc_add(dk0, st * C::kTile);
@@ -558,14 +246,14 @@ __device__ void multiply(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, u
     tc::commit(tc::smem_u32(&sh.kempty[st]));
   };
   for (w.start(a, s, sh.share); ok && w.left > 0; w.next(a, s), ++piece) {
-    ok = kv_wait(sh, sh.qfull, piece & 1u);
+    ok = kv_wait(&sh.abort, sh.qfull, piece & 1u);
     if (!ok) break;
     scores(n);
     for (int i = 0; ok && i < w.take; ++i, ++n) {
       if (i + 1 < w.take) scores(n + 1);
       const int st = (int)(n % C::kStages);
-      ok = ok && kv_wait(sh, sh.vfull[st], (uint32_t)(n / C::kStages) & 1u) &&
-           kv_wait(sh, sh.pfull, (uint32_t)n & 1u);
+      ok = ok && kv_wait(&sh.abort, sh.vfull[st], (uint32_t)(n / C::kStages) & 1u) &&
+           kv_wait(&sh.abort, sh.pfull, (uint32_t)n & 1u);
       if (!ok) break;
       tc::fence_after_sync();
       const uint64_t dv = tc::desc_add(dv0, st * C::kTile);
@@ -694,8 +382,8 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
     const int64_t all_lo64 = a.window > 0 ? (int64_t)w.x.pos0 + last_q + 1 - a.window : 0;
     for (int i = 0; i < w.take; ++i, ++n) {
       const int st = (int)(n % C::kStages);
-      bad |= !kv_wait(sh, sh.sfull[n & 1], (uint32_t)(n >> 1) & 1u);
-      bad |= !kv_wait(sh, sh.vfull[st], (uint32_t)(n / C::kStages) & 1u);
+      bad |= !kv_wait(&sh.abort, sh.sfull[n & 1], (uint32_t)(n >> 1) & 1u);
+      bad |= !kv_wait(&sh.abort, sh.vfull[st], (uint32_t)(n / C::kStages) & 1u);
       tc::fence_after_sync();
       float u[CW];
       {
@@ -758,7 +446,7 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
         const float top = warp_columns<CW, true>(t, lane);
         if (lane < CW) sh.red[wg][wq][lane] = top;
         asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
-        if (i > 0) bad |= !kv_wait(sh, sh.pvdone, (uint32_t)(n - 1) & 1u);
+        if (i > 0) bad |= !kv_wait(&sh.abort, sh.pvdone, (uint32_t)(n - 1) & 1u);
         tc::fence_after_sync();
         float f[CW];
 #pragma unroll
@@ -785,7 +473,7 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
         }
         asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");  // red may be written again
       } else if (i > 0) {
-        bad |= !kv_wait(sh, sh.pvdone, (uint32_t)(n - 1) & 1u);  // P may be written again
+        bad |= !kv_wait(&sh.abort, sh.pvdone, (uint32_t)(n - 1) & 1u);  // P may be written again
       }
       uint32_t dig[3][CW / 4];
 #pragma unroll
@@ -829,7 +517,7 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
       tc::fence_before_sync();
       tc::mbar_arrive(tc::smem_u32(&sh.pfull));
     }
-    if (!bad) bad = !kv_wait(sh, sh.pvdone, (uint32_t)(n - 1) & 1u);
+    if (!bad) bad = !kv_wait(&sh.abort, sh.pvdone, (uint32_t)(n - 1) & 1u);
     if (tc::named_sync_or(3, C::kSoft, bad)) break;
     tc::fence_after_sync();
     // sums over the keys: the warp's rows, then the four warps
@@ -846,8 +534,8 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
       for (int c = 0; c < CW; ++c) mm = row == c ? m[c] : mm;
       const int64_t to = sh.col_row[c0 + row];
       if (whole) {
-        sh.linv[c0 + row] = tot > 0.0f ? __fdiv_rn(1.0f, tot) : 0.0f;
-        if (a.lse && to >= 0) a.lse[to] = tot > 0.0f ? (mm + log2f(tot) - kLift) * kLn2 : -INFINITY;
+        sh.linv[c0 + row] = tot != 0.0f ? __fdiv_rn(1.0f, tot) : 0.0f;
+        if (a.lse && to >= 0) a.lse[to] = tot != 0.0f ? (mm + log2f(tot) - kLift) * kLn2 : -INFINITY;
       } else {
         part[C::NC * C::kHD + 2 * (c0 + row)] = mm;
         part[C::NC * C::kHD + 2 * (c0 + row) + 1] = tot;
@@ -951,76 +639,18 @@ __global__ void __launch_bounds__(C::kThreads) kv8_attn_kernel(const __grid_cons
   if (tid == 0 && sh.abort) flag(a.status, CSA2_DEV_TIMEOUT);
 }
 
-// Joins the pieces of the item that CTA blockIdx.x starts and does not end: with M the largest
-// of the pieces' maxima, out = sum 2^(m - M) O / sum 2^(m - M) l.  blockIdx.y: 8 columns; a
-// thread one channel of them.
-template <class C, typename T>
-__global__ void __launch_bounds__(C::kHD) kv8_merge_kernel(const KvAttnArgs a, int ctas) {
-  chain_enter();
-  const int cta = blockIdx.x, c0 = blockIdx.y * 8, d = threadIdx.x;
-  const int32_t* meta = a.meta + (int64_t)cta * kMetaInts;
-  if (meta[1] == 0) return;
-  const Shape s = shape_of<C::NC>(a);
-  const int r = meta[2], hh = meta[3], qb = meta[4];
-  uint32_t bad = 0;
-  const Request x = request_of(a, s, r, &bad);
-  constexpr int kPart = C::NC * (C::kHD + 2);
-  float M[8], l[8], o[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    M[j] = -INFINITY;
-    l[j] = 0.0f;
-    o[j] = 0.0f;
-  }
-  for (int k = cta; k < ctas; ++k) {
-    const bool mine = k == cta;
-    const int state = mine ? 1 : a.meta[(int64_t)k * kMetaInts];
-    if (state == 0) continue;  // a CTA without work
-    const float* p = a.part + ((int64_t)k * 2 + (mine ? 1 : 0)) * kPart;
-    float po[8];
-    float2 ml[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      po[j] = p[(c0 + j) * C::kHD + d];
-      ml[j] = *reinterpret_cast<const float2*>(p + C::NC * C::kHD + 2 * (c0 + j));
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (ml[j].y > 0.0f) {  // a piece that saw no key has no maximum
-        const float top = fmaxf(M[j], ml[j].x), fa = exp2f(M[j] - top), fb = exp2f(ml[j].x - top);
-        l[j] = l[j] * fa + ml[j].y * fb;
-        o[j] = o[j] * fa + po[j] * fb;
-        M[j] = top;
-      }
-    }
-    if (state == 2) break;
-  }
-  const int hb = hh % s.nhb;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int c = c0 + j, qi = c / s.HB, hd = c - qi * s.HB, i = qb * s.QB + qi;
-    if (qi >= s.QB || i >= x.n || hd >= s.G - hb * s.HB) continue;
-    const int64_t to = (int64_t)(x.q0 + i) * a.Hq + hh / s.nhb * s.G + hb * s.HB + hd;
-    reinterpret_cast<T*>(a.out)[to * C::kHD + d] = from_float<T>(l[j] > 0.0f ? o[j] / l[j] : 0.0f);
-    if (a.lse && d == 0) a.lse[to] = l[j] > 0.0f ? (M[j] + log2f(l[j]) - kLift) * kLn2 : -INFINITY;
-  }
-}
-
 // ---- host --------------------------------------------------------------------------------
-// Columns per tile: the smallest of 8, 16, 32, 64 that holds a request's queries times the
-// heads of a group, so decode pays for no empty columns and long chunks share each tile's
-// keys most; fp16 queries stop at 32 (three digits of 64 columns exceed the tensor memory).
-static int columns_of(int Hq, int Hk, int max_q, int f16) {
-  const int64_t want = (int64_t)(Hq / Hk) * (max_q < 1 ? 1 : max_q);
-  const int most = f16 ? 32 : 64;
-  int nc = 8;
-  while (nc < most && nc < want) nc *= 2;
-  return nc;
+// Columns per tile: the smallest of 8, 16, 32 that holds a request's queries times the heads of
+// a group, so decode pays for no empty columns; beyond that the f16 kernel (0).
+static int columns_of(int Hq, int Hk, int max_q) {
+  const int64_t want = (int64_t)(Hq / Hk) * max_q;
+  return want <= 8 ? 8 : want <= 16 ? 16 : want <= kMaxColumns ? 32 : 0;
 }
 static int ctas_of(int nc, int num_sms) { return num_sms * (nc <= 16 ? 2 : 1); }
 
-size_t kv8_attn_workspace_bytes(int Hq, int Hk, int hd, int max_q, int f16, int num_sms) {
-  const int nc = columns_of(Hq, Hk, max_q, f16), ctas = ctas_of(nc, num_sms);
+size_t kv8_attn_workspace_bytes(int Hq, int Hk, int hd, int max_q, int num_sms) {
+  const int nc = columns_of(Hq, Hk, max_q), ctas = ctas_of(nc, num_sms);
+  if (nc == 0) return kv8_wide_workspace_bytes(hd, num_sms);
   return (size_t)ctas * 2 * nc * (hd + 2) * sizeof(float) + (size_t)ctas * kMetaInts * sizeof(int32_t);
 }
 
@@ -1041,14 +671,15 @@ static EncodeFn encode_fn() {
 }
 
 // The cache as rows of hd bytes; a box is one head's rows of one page.
-static bool encode_rows(CUtensorMap* m, const uint8_t* cache, int64_t rows, int hd, int page) {
+static bool encode_rows(CUtensorMap* m, const uint8_t* cache, int64_t rows, int hd, int page, bool swizzle) {
   const EncodeFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)hd, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)hd};
   const cuuint32_t box[2] = {(cuuint32_t)hd, (cuuint32_t)page}, one[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(cache), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1062,7 +693,7 @@ static cudaError_t launch_kv8_t(const CUtensorMap& km, const CUtensorMap& vm, Kv
   if (e != cudaSuccess) return e;
   e = launch_chained(kv8_attn_kernel<C, T>, dim3(ctas), dim3(C::kThreads), C::kSmem, stream, 0, km, vm, a);
   if (e != cudaSuccess) return e;
-  e = launch_chained(kv8_merge_kernel<C, T>, dim3(ctas, C::NC / 8), dim3(C::kHD), 0, stream, 0, a, ctas);
+  e = launch_chained(kv8_merge_kernel<C::NC, C::kHD, T>, dim3(ctas, C::NC / 8), dim3(C::kHD), 0, stream, 0, a, ctas, kLift);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -1071,9 +702,7 @@ static cudaError_t launch_kv8_nc(int nc, const CUtensorMap& km, const CUtensorMa
                                  int num_sms, cudaStream_t stream) {
   if (nc == 8) return launch_kv8_t<KvCfg<HD, 8, DQ, CAP>, T>(km, vm, a, ws, num_sms, stream);
   if (nc == 16) return launch_kv8_t<KvCfg<HD, 16, DQ, CAP>, T>(km, vm, a, ws, num_sms, stream);
-  if (nc == 32) return launch_kv8_t<KvCfg<HD, 32, DQ, CAP>, T>(km, vm, a, ws, num_sms, stream);
-  if constexpr (DQ == 2) return launch_kv8_t<KvCfg<HD, 64, DQ, CAP>, T>(km, vm, a, ws, num_sms, stream);
-  return cudaErrorInvalidValue;
+  return launch_kv8_t<KvCfg<HD, 32, DQ, CAP>, T>(km, vm, a, ws, num_sms, stream);
 }
 
 template <int HD, bool CAP>
@@ -1111,9 +740,10 @@ cudaError_t launch_kv8_attn(const void* q, int64_t q_stride, int f16, int64_t T,
   a.status = status;
   CUtensorMap km, vm;
   const int64_t rows = n_pages * Hk * page;
-  if (!encode_rows(&km, k_cache, rows, hd, page) || !encode_rows(&vm, v_cache, rows, hd, page))
+  const int nc = columns_of(Hq, Hk, max_q);
+  if (!encode_rows(&km, k_cache, rows, hd, page, nc > 0) || !encode_rows(&vm, v_cache, rows, hd, page, nc > 0))
     return cudaErrorInvalidValue;
-  const int nc = columns_of(Hq, Hk, max_q, f16);
+  if (nc == 0) return launch_kv8_wide(a, f16, hd, km, vm, ws, num_sms, stream);
   if (hd == 64)
     return softcap > 0.0f ? launch_kv8_type<64, true>(f16, nc, km, vm, a, ws, num_sms, stream)
                           : launch_kv8_type<64, false>(f16, nc, km, vm, a, ws, num_sms, stream);

@@ -1,0 +1,415 @@
+// What the attention kernels of the paged 8-bit KV cache share: their arguments, the list of key
+// tiles that the CTAs split evenly, bounded waits, and the kernel that joins split items.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "csa2_device.cuh"
+#include "kv8.cuh"
+#include "tc.cuh"
+
+namespace csa2 {
+
+constexpr int kKeys = 128;             // keys per tile
+constexpr int kMaxTilePages = 8;       // pages of 16 rows
+constexpr float kSlack = 2.0f;         // the running maximum is raised when exceeded by more (base 2)
+constexpr uint32_t kKvPolls = 1u << 22;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct KvAttnArgs {
+  const uint8_t* q;
+  int64_t q_stride;  // bytes from token to token
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* table;
+  const int32_t* q_start;
+  const int32_t* seq_len;
+  int R, Hq, Hk, max_pages, page_log2;
+  int64_t n_pages;
+  int64_t T;
+  float sm_scale;
+  int window;
+  float softcap;
+  uint8_t* out;
+  float* lse;
+  float* part;    // [CTA][2][NC][hd + 2]
+  int32_t* meta;  // [CTA][8]
+  uint32_t* status;
+};
+
+// Partial results of CTA c: slot 0 the piece that continues an item, slot 1 the one that
+// starts an item and does not end it.  meta: [0] slot 0 (0 none, 1 goes on, 2 ends the item),
+// [1] slot 1 used, [2..5] its request, head, head block, query block.
+constexpr int kMetaInts = 8;
+
+// Rows of hd bytes from `row` on (a box of the map) into shared memory.
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(map), "r"(0), "r"(row), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+
+// ---- the list of key tiles -------------------------------------------------------------
+struct Request {
+  int q0, n;     // first query row, queries
+  int pos0;      // position of the first query
+  int cap;       // keys: min(seq_len, what the table holds)
+  int nqb;       // query blocks
+};
+struct Shape {   // how a request's columns are cut
+  int G, QB, HB, nhb;
+};
+template <int NC>
+__device__ __forceinline__ Shape shape_of(const KvAttnArgs& a) {
+  Shape s;
+  s.G = a.Hq / a.Hk;
+  s.HB = s.G < NC ? s.G : NC;
+  s.QB = s.G < NC ? NC / s.G : 1;
+  s.nhb = (s.G + NC - 1) / NC;
+  return s;
+}
+__device__ __forceinline__ Request request_of(const KvAttnArgs& a, const Shape& s, int r, uint32_t* bad) {
+  Request x;
+  const int64_t b = a.q_start[r], e = a.q_start[r + 1];
+  int len = a.seq_len[r];
+  const int64_t q0 = b < 0 ? 0 : (b < a.T ? b : a.T), q1 = e < q0 ? q0 : (e < a.T ? e : a.T);
+  if (q0 != b || q1 != e || len < 0) *bad |= CSA2_DEV_BAD_COUNT;
+  if (len < 0) len = 0;
+  x.q0 = (int)q0;
+  x.n = (int)(q1 - q0);
+  if (x.n > len) *bad |= CSA2_DEV_BAD_COUNT;
+  x.pos0 = len - x.n;
+  const int64_t held = (int64_t)a.max_pages << a.page_log2;
+  if (len > held) *bad |= CSA2_DEV_BAD_COUNT;
+  x.cap = len < held ? len : (int)held;
+  x.nqb = (x.n + s.QB - 1) / s.QB;
+  return x;
+}
+// Keys [lo, hi) that any query of block qb sees, and its first tile and number of tiles (at
+// least one: a block that sees nothing still writes its rows).
+struct Range {
+  int lo, hi, tile, tiles;
+};
+__device__ __forceinline__ Range range_of(const KvAttnArgs& a, const Shape& s, const Request& x, int qb) {
+  Range g;
+  const int i0 = qb * s.QB, i1 = i0 + s.QB < x.n ? i0 + s.QB : x.n;
+  const int64_t hi = (int64_t)x.pos0 + i1;
+  g.hi = hi < 0 ? 0 : (hi < x.cap ? (int)hi : x.cap);
+  const int64_t lo = a.window > 0 ? (int64_t)x.pos0 + i0 + 1 - a.window : 0;
+  g.lo = lo < 0 ? 0 : (lo < g.hi ? (int)lo : g.hi);
+  g.tile = g.lo / kKeys;
+  const int end = (g.hi + kKeys - 1) / kKeys;
+  g.tiles = end > g.tile ? end - g.tile : 1;
+  return g;
+}
+// Tiles of one (request, key head, head block).
+__device__ __forceinline__ int64_t row_tiles(const KvAttnArgs& a, const Shape& s, const Request& x, int first, int step) {
+  int64_t n = 0;
+  for (int qb = first; qb < x.nqb; qb += step) n += range_of(a, s, x, qb).tiles;
+  return n;
+}
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// row_tiles of request r for each lane (r < R where live), long requests by the whole warp.
+__device__ __forceinline__ int64_t lane_row_tiles(const KvAttnArgs& a, const Shape& s, int r, bool live, int lane,
+                                                  uint32_t* bad) {
+  Request x = {};
+  if (live) x = request_of(a, s, r, bad);
+  const bool big = x.nqb > 8;
+  int64_t n = big ? 0 : row_tiles(a, s, x, 0, 1);
+  unsigned todo = __ballot_sync(0xffffffffu, big);
+  while (todo) {
+    const int src = __ffs(todo) - 1;
+    todo &= todo - 1;
+    Request y;
+    y.q0 = __shfl_sync(0xffffffffu, x.q0, src);
+    y.n = __shfl_sync(0xffffffffu, x.n, src);
+    y.pos0 = __shfl_sync(0xffffffffu, x.pos0, src);
+    y.cap = __shfl_sync(0xffffffffu, x.cap, src);
+    y.nqb = __shfl_sync(0xffffffffu, x.nqb, src);
+    const int64_t m = warp_sum(row_tiles(a, s, y, lane, 32));
+    if (lane == src) n = m;
+  }
+  return n;
+}
+
+// This CTA's share of the list: its length, and where it begins.
+struct Share {
+  int64_t left;
+  int r, hh, qb, off;  // request, key head * nhb + head block, query block, tile inside the item
+};
+
+// A walk over a share's pieces; every role keeps its own.
+struct Walk {
+  int64_t left;
+  int r, hh, qb, off;
+  Request x;
+  Range g;
+  int take;        // tiles of this piece
+  bool first, last;
+  __device__ __forceinline__ void open(const KvAttnArgs& a, const Shape& s) {
+    g = range_of(a, s, x, qb);
+    const int rest = g.tiles - off;
+    take = left < rest ? (int)left : rest;
+    first = off == 0;
+    last = off + take == g.tiles;
+  }
+  __device__ __forceinline__ void start(const KvAttnArgs& a, const Shape& s, const Share& w) {
+    left = w.left;
+    r = w.r;
+    hh = w.hh;
+    qb = w.qb;
+    off = w.off;
+    if (left <= 0) return;
+    uint32_t bad = 0;
+    x = request_of(a, s, r, &bad);
+    open(a, s);
+  }
+  __device__ __forceinline__ void next(const KvAttnArgs& a, const Shape& s) {
+    left -= take;
+    off = 0;
+    if (left <= 0) return;
+    if (++qb < x.nqb) {
+      open(a, s);
+      return;
+    }
+    qb = 0;
+    if (++hh < a.Hk * s.nhb) {
+      open(a, s);
+      return;
+    }
+    hh = 0;
+    uint32_t bad = 0;
+    do {
+      if (++r >= a.R) {  // cannot happen while left > 0
+        left = 0;
+        return;
+      }
+      x = request_of(a, s, r, &bad);
+    } while (x.n == 0);
+    open(a, s);
+  }
+};
+
+// Computed by the whole CTA (kThreads threads); `sums` holds a value per thread.
+template <int kThreads>
+__device__ void find_share(const KvAttnArgs& a, const Shape& s, int64_t* sums, Share* out, uint32_t* bad) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int per = (a.R + kThreads - 1) / kThreads;  // requests per thread, consecutive
+  const int heads = a.Hk * s.nhb;
+  int64_t mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int r = tid * per + i;
+    mine += lane_row_tiles(a, s, r, r < a.R, lane, bad);
+  }
+  sums[tid] = mine * heads;
+  __syncthreads();
+  if (tid < 32) {
+    constexpr int kEach = kThreads / 32;
+    int64_t part = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) part += sums[lane * kEach + i];
+    int64_t upto = part;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+    const int64_t c = blockIdx.x, C = gridDim.x;
+    const int64_t t0 = total / C * c + total % C * c / C, t1 = total / C * (c + 1) + total % C * (c + 1) / C;
+    Share w = {t1 - t0, 0, 0, 0, 0};
+    if (w.left > 0) {
+      // the thread whose requests hold tile t0 ...
+      const unsigned m = __ballot_sync(0xffffffffu, upto > t0);
+      const int l0 = __ffs(m) - 1;
+      int64_t before = __shfl_sync(0xffffffffu, upto - part, l0);
+      int th = l0 * kEach;
+      while (before + sums[th] <= t0) before += sums[th++];
+      // ... the request (32 at a time) ...
+      int64_t rest = t0 - before;
+      int r = th * per;
+      Request x;
+      int64_t row;
+      for (;;) {
+        const int64_t n = lane_row_tiles(a, s, r + lane, r + lane < a.R, lane, bad) * heads;
+        int64_t in = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, in, o);
+          if (lane >= o) in += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, in > rest);
+        if (hit) {
+          const int l = __ffs(hit) - 1;
+          rest -= __shfl_sync(0xffffffffu, in - n, l);
+          row = __shfl_sync(0xffffffffu, n, l) / heads;
+          r += l;
+          break;
+        }
+        rest -= __shfl_sync(0xffffffffu, in, 31);
+        r += 32;
+      }
+      x = request_of(a, s, r, bad);
+      w.r = r;
+      w.hh = (int)(rest / row);
+      rest -= (int64_t)w.hh * row;
+      // ... and the query block
+      for (int qb0 = 0;; qb0 += 32) {
+        const int n = qb0 + lane < x.nqb ? range_of(a, s, x, qb0 + lane).tiles : 0;
+        int64_t in = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, in, o);
+          if (lane >= o) in += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, in > rest);
+        if (hit) {
+          const int l = __ffs(hit) - 1;
+          w.qb = qb0 + l;
+          w.off = (int)(rest - __shfl_sync(0xffffffffu, in - n, l));
+          break;
+        }
+        rest -= __shfl_sync(0xffffffffu, in, 31);
+        if (qb0 + 32 >= x.nqb) break;  // cannot happen
+      }
+    }
+    if (lane == 0) *out = w;
+  }
+  __syncthreads();
+}
+
+// Bounded wait that also ends when another role of the CTA has given up (*abort != 0).
+__device__ __forceinline__ bool kv_wait(int* abort, uint64_t& bar, uint32_t parity) {
+  const uint32_t b = tc::smem_u32(&bar);
+  uint64_t t0 = 0;
+  for (uint32_t i = 0; i < kKvPolls; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(b), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 63u) == 63u) {
+      if (*reinterpret_cast<volatile int*>(abort)) return false;
+      const uint64_t now = tc::globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > tc::kWaitLimitNs) break;
+    }
+  }
+  *reinterpret_cast<volatile int*>(abort) = 1;
+  return false;
+}
+
+// Joins the pieces of the item that CTA blockIdx.x starts and does not end: with M the largest
+// of the pieces' maxima, out = sum 2^(m - M) O / sum 2^(m - M) l.  blockIdx.y: 8 columns; a
+// thread one channel of them.  The pieces' count and weights come first (a lane per piece), so
+// the sums over the pieces are independent loads.
+template <int NC, int HD, typename T>
+__global__ void __launch_bounds__(HD) kv8_merge_kernel(const KvAttnArgs a, int ctas, float lift) {
+  constexpr int kChunk = 64, kPart = NC * (HD + 2), kWarps = HD / 32;
+  __shared__ int s_end;
+  __shared__ float s_w[kChunk][8], s_m[8], s_l[8];
+  chain_enter();
+  const int cta = blockIdx.x, c0 = blockIdx.y * 8, d = threadIdx.x, lane = d & 31, warp = d >> 5;
+  const int32_t* meta = a.meta + (int64_t)cta * kMetaInts;
+  if (meta[1] == 0) return;
+  if (d == 0) s_end = ctas;
+  __syncthreads();
+  for (int base = cta + 1; base < ctas; base += HD) {  // the piece that ends the item
+    const int k = base + d;
+    if (k < ctas && a.meta[(int64_t)k * kMetaInts] == 2) atomicMin(&s_end, k);
+    __syncthreads();
+    if (s_end < ctas) break;
+  }
+  const int n = (s_end < ctas ? s_end + 1 : ctas) - cta;  // piece i is CTA cta + i's
+  const auto piece = [&](int i) { return a.part + ((int64_t)(cta + i) * 2 + (i == 0 ? 1 : 0)) * kPart; };
+  const auto stats = [&](int i, int j) {  // maximum and sum; (0, 0) of a CTA without work
+    if (i > 0 && a.meta[(int64_t)(cta + i) * kMetaInts] == 0) return make_float2(0.0f, 0.0f);
+    return *reinterpret_cast<const float2*>(piece(i) + NC * HD + 2 * (c0 + j));
+  };
+  for (int j = warp; j < 8; j += kWarps) {
+    float M = -INFINITY, l = 0.0f;
+    for (int i = lane; i < n; i += 32) {
+      const float2 s = stats(i, j);
+      if (s.y != 0.0f) M = fmaxf(M, s.x);  // a piece that saw no key has no maximum
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int i = lane; i < n; i += 32) {
+      const float2 s = stats(i, j);
+      if (s.y != 0.0f) l += s.y * exp2f(s.x - M);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) {
+      s_m[j] = M;
+      s_l[j] = l;
+    }
+  }
+  float acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+  for (int i0 = 0; i0 < n; i0 += kChunk) {
+    const int in = n - i0 < kChunk ? n - i0 : kChunk;
+    __syncthreads();
+    for (int x = d; x < in * 8; x += HD) {
+      const float2 s = stats(i0 + x / 8, x % 8);
+      s_w[x / 8][x % 8] = s.y != 0.0f ? exp2f(s.x - s_m[x % 8]) : 0.0f;
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int i = 0; i < in; ++i) {
+      const float* p = piece(i0 + i) + c0 * HD + d;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float w = s_w[i][j];
+        if (w != 0.0f) acc[j] = fmaf(p[j * HD], w, acc[j]);  // what holds nothing was not written
+      }
+    }
+  }
+  const Shape s = shape_of<NC>(a);
+  const int r = meta[2], hh = meta[3], qb = meta[4], hb = hh % s.nhb;
+  uint32_t bad = 0;
+  const Request x = request_of(a, s, r, &bad);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int c = c0 + j, qi = c / s.HB, hd = c - qi * s.HB, i = qb * s.QB + qi;
+    if (qi >= s.QB || i >= x.n || hd >= s.G - hb * s.HB) continue;
+    const int64_t to = (int64_t)(x.q0 + i) * a.Hq + hh / s.nhb * s.G + hb * s.HB + hd;
+    const float l = s_l[j];
+    reinterpret_cast<T*>(a.out)[to * HD + d] = from_float<T>(l != 0.0f ? __fdiv_rn(acc[j], l) : 0.0f);
+    if (a.lse && d == 0) a.lse[to] = l != 0.0f ? (s_m[j] + log2f(l) - lift) * kLn2 : -INFINITY;
+  }
+}
+
+// kv8_wide.cu: the kernel for many rows per key head.
+size_t kv8_wide_workspace_bytes(int hd, int num_sms);
+cudaError_t launch_kv8_wide(const KvAttnArgs& a, int f16, int hd, const CUtensorMap& km, const CUtensorMap& vm, void* ws,
+                            int num_sms, cudaStream_t stream);
+
+}  // namespace csa2
