@@ -505,65 +505,88 @@ def csa2_attn_combine(out_parts, lse_parts, out, lse, stream=None):
 
 
 # ---- paged 8-bit KV cache ----------------------------------------------------------------
-_KV_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+# These calls are made per layer of a decode step, where the host's time shows: their checks
+# read each tensor's properties once and explain a refusal only when there is one.
+_BF16, _F16, _I32, _I64, _F32, _U8 = (torch.bfloat16, torch.float16, torch.int32, torch.int64, torch.float32, torch.uint8)
+_KV_DTYPES = {_BF16: 0, _F16: 1}
+
+
+def _refuse(t, dtype, shape, name, dev):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _arg(t, dtype, shape, name, dev):
-    """Raise unless t is a contiguous `dtype` tensor of exactly `shape` on `dev`; its address."""
-    if not (t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()):
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
-        raise ValueError(f"{name} must be contiguous")
+    """Raise unless t is a contiguous `dtype` tensor of exactly `shape` on cuda:`dev`; its address."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, dtype, shape, name, dev)
     return t.data_ptr()
 
 
 def _tokens(t, dtype, shape, name, dev):
     """The same for a [T, heads, hd] view whose tokens are each contiguous: (address, token stride)."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    row = shape[1] * shape[2]
-    st = t.stride()
-    if shape[0] > 0 and ((st[2] != 1) or (st[1] != shape[2] and shape[1] > 1)):
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, dtype, shape, name, dev)
+    T, heads, hd = shape
+    s0, s1, s2 = t.stride()
+    if T > 0 and (s2 != 1 or (s1 != hd and heads > 1)):
         raise ValueError(f"{name}: each token's [heads, hd] must be contiguous")
-    if shape[0] <= 1:
-        return t.data_ptr(), row
-    if st[0] < row or st[0] % 8:
+    if T <= 1:
+        return t.data_ptr(), heads * hd
+    if s0 < heads * hd or s0 % 8:
         raise ValueError(f"{name}: the token stride must be a multiple of 8 elements and at least heads * hd")
-    return t.data_ptr(), st[0]
+    return t.data_ptr(), s0
 
 
 def _flag_arg(dev_status, dev):
     if dev_status is None:
         return None
-    if dev_status.dtype is not torch.int32 or dev_status.numel() < 1 or dev_status.device != dev:
-        raise ValueError(f"dev_status must be an int32 tensor with at least one element on {dev}")
+    if dev_status.dtype is not _I32 or dev_status.numel() < 1 or dev_status.get_device() != dev:
+        raise ValueError(f"dev_status must be an int32 tensor with at least one element on cuda:{dev}")
     return dev_status.data_ptr()
 
 
 def _cuda_dev(t, name):
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return dev
+
+
+def _length(t, name):
+    sh = t.shape
+    if len(sh) != 1:
+        raise ValueError(f"{name} must be 1-D, got {tuple(sh)}")
+    return sh[0]
+
+
+def _table(t, R, dev):
+    """(address, columns) of the block table of R requests."""
+    sh = t.shape
+    if len(sh) != 2:
+        raise ValueError(f"block_table must be 2-D, got {tuple(sh)}")
+    return _arg(t, _I32, (R, sh[1]), "block_table", dev), sh[1]
 
 
 def _call_on(dev, stream, fn, *args):
-    """fn(*args, stream) with `dev` current (the library launches on the current device)."""
+    """fn(*args, stream) with cuda:`dev` current (the library launches on the current device)."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
-    if torch.cuda.current_device() == dev.index:
-        return fn(*args, stream.cuda_stream)
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{dev}")
+    else:
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        return fn(*args, raw)
     with torch.cuda.device(dev):
-        return fn(*args, stream.cuda_stream)
+        return fn(*args, raw)
 
 
 def csa2_paged_plan(ctx_len, new_len, block_table, free_pages, n_free, page, n_pages, seq_len, n_free_out, q_start,
@@ -573,19 +596,14 @@ def csa2_paged_plan(ctx_len, new_len, block_table, free_pages, n_free, page, n_p
     q_start i32 [R+1], slot_map and pos i64 [T_cap] (see include/csa2.h).  seq_len may be
     ctx_len and n_free_out may be n_free."""
     dev = _cuda_dev(ctx_len, "ctx_len")
-    _shape(ctx_len, (None,), "ctx_len")
-    _shape(block_table, (ctx_len.shape[0], None), "block_table")
-    _shape(free_pages, (None,), "free_pages")
-    _shape(slot_map, (None,), "slot_map")
-    R, T, i32, i64 = ctx_len.shape[0], slot_map.shape[0], torch.int32, torch.int64
+    R, F, T = _length(ctx_len, "ctx_len"), _length(free_pages, "free_pages"), _length(slot_map, "slot_map")
+    ta, cols = _table(block_table, R, dev)
     _check(_call_on(
-        dev, stream, lib().csa2_paged_plan, _arg(ctx_len, i32, (R,), "ctx_len", dev),
-        _arg(new_len, i32, (R,), "new_len", dev), R, page,
-        _arg(block_table, i32, block_table.shape, "block_table", dev), block_table.shape[1],
-        _arg(free_pages, i32, free_pages.shape, "free_pages", dev), free_pages.shape[0],
-        _arg(n_free, i32, (1,), "n_free", dev), n_pages, _arg(seq_len, i32, (R,), "seq_len", dev),
-        _arg(n_free_out, i32, (1,), "n_free_out", dev), _arg(q_start, i32, (R + 1,), "q_start", dev),
-        _arg(slot_map, i64, (T,), "slot_map", dev), _arg(pos, i64, (T,), "pos", dev), T, _flag_arg(dev_status, dev)),
+        dev, stream, lib().csa2_paged_plan, _arg(ctx_len, _I32, (R,), "ctx_len", dev),
+        _arg(new_len, _I32, (R,), "new_len", dev), R, page, ta, cols, _arg(free_pages, _I32, (F,), "free_pages", dev), F,
+        _arg(n_free, _I32, (1,), "n_free", dev), n_pages, _arg(seq_len, _I32, (R,), "seq_len", dev),
+        _arg(n_free_out, _I32, (1,), "n_free_out", dev), _arg(q_start, _I32, (R + 1,), "q_start", dev),
+        _arg(slot_map, _I64, (T,), "slot_map", dev), _arg(pos, _I64, (T,), "pos", dev), T, _flag_arg(dev_status, dev)),
         "csa2_paged_plan")
 
 
@@ -595,26 +613,23 @@ def csa2_paged_release(seq_len, block_table, release, free_pages, n_free, page, 
     after its n_free i32 [1] entries; seq_len_out i32 [R] (0 for those) and n_free_out i32 [1]
     may be seq_len and n_free."""
     dev = _cuda_dev(seq_len, "seq_len")
-    _shape(seq_len, (None,), "seq_len")
-    _shape(block_table, (seq_len.shape[0], None), "block_table")
-    _shape(free_pages, (None,), "free_pages")
-    R, i32 = seq_len.shape[0], torch.int32
+    R, F = _length(seq_len, "seq_len"), _length(free_pages, "free_pages")
+    ta, cols = _table(block_table, R, dev)
     _check(_call_on(
-        dev, stream, lib().csa2_paged_release, _arg(seq_len, i32, (R,), "seq_len", dev),
-        _arg(block_table, i32, block_table.shape, "block_table", dev),
-        _arg(release, torch.uint8, (R,), "release", dev), R, page, block_table.shape[1],
-        _arg(free_pages, i32, free_pages.shape, "free_pages", dev), free_pages.shape[0],
-        _arg(n_free, i32, (1,), "n_free", dev), n_pages, _arg(seq_len_out, i32, (R,), "seq_len_out", dev),
-        _arg(n_free_out, i32, (1,), "n_free_out", dev), _flag_arg(dev_status, dev)), "csa2_paged_release")
+        dev, stream, lib().csa2_paged_release, _arg(seq_len, _I32, (R,), "seq_len", dev), ta,
+        _arg(release, _U8, (R,), "release", dev), R, page, cols, _arg(free_pages, _I32, (F,), "free_pages", dev), F,
+        _arg(n_free, _I32, (1,), "n_free", dev), n_pages, _arg(seq_len_out, _I32, (R,), "seq_len_out", dev),
+        _arg(n_free_out, _I32, (1,), "n_free_out", dev), _flag_arg(dev_status, dev)), "csa2_paged_release")
 
 
 def _cache_args(k_cache, v_cache, k_scale, v_scale, dev):
     """(n_pages, Hk, page, hd) and the four addresses of one layer's cache."""
-    _shape(k_cache, (None, None, None, None), "k_cache")
     sh = k_cache.shape
-    return sh, (_arg(k_cache, torch.uint8, sh, "k_cache", dev), _arg(v_cache, torch.uint8, sh, "v_cache", dev),
-                _arg(k_scale, torch.float32, sh[:2], "k_scale", dev),
-                _arg(v_scale, torch.float32, sh[:2], "v_scale", dev))
+    if len(sh) != 4:
+        raise ValueError(f"k_cache must be [n_pages, Hk, page, hd], got {tuple(sh)}")
+    per = (sh[0], sh[1])
+    return sh, (_arg(k_cache, _U8, sh, "k_cache", dev), _arg(v_cache, _U8, sh, "v_cache", dev),
+                _arg(k_scale, _F32, per, "k_scale", dev), _arg(v_scale, _F32, per, "v_scale", dev))
 
 
 def csa2_kv8_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, dev_status=None, stream=None):
@@ -623,13 +638,15 @@ def csa2_kv8_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, dev_stat
     per page and head in k_scale, v_scale f32 [n_pages,Hk] (see include/csa2.h)."""
     dev = _cuda_dev(k, "k")
     (P, Hk, page, hd), cache = _cache_args(k_cache, v_cache, k_scale, v_scale, dev)
-    if k.dtype not in _KV_DTYPES:
-        raise TypeError(f"k must be bfloat16 or float16, got {k.dtype}")
-    T = k.shape[0] if k.dim() else 0
-    ka, ks = _tokens(k, k.dtype, (T, Hk, hd), "k", dev)
-    va, vs = _tokens(v, k.dtype, (T, Hk, hd), "v", dev)
-    _check(_call_on(dev, stream, lib().csa2_kv8_append, ka, va, ks, vs, _KV_DTYPES[k.dtype], T, Hk, hd,
-                    _arg(slot_map, torch.int64, (T,), "slot_map", dev), *cache, P, page, _flag_arg(dev_status, dev)),
+    dtype = k.dtype
+    if dtype not in _KV_DTYPES:
+        raise TypeError(f"k must be bfloat16 or float16, got {dtype}")
+    T = _length(slot_map, "slot_map")
+    rows = (T, Hk, hd)
+    ka, ks = _tokens(k, dtype, rows, "k", dev)
+    va, vs = _tokens(v, dtype, rows, "v", dev)
+    _check(_call_on(dev, stream, lib().csa2_kv8_append, ka, va, ks, vs, _KV_DTYPES[dtype], T, Hk, hd,
+                    _arg(slot_map, _I64, (T,), "slot_map", dev), *cache, P, page, _flag_arg(dev_status, dev)),
            "csa2_kv8_append")
 
 
@@ -644,29 +661,33 @@ def csa2_kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, q_start, s
     (contiguous) and lse f32 [T,Hq] or None (see include/csa2.h)."""
     dev = _cuda_dev(q, "q")
     (P, Hk, page, hd), cache = _cache_args(k_cache, v_cache, k_scale, v_scale, dev)
-    if q.dtype not in _KV_DTYPES:
-        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
-    _shape(q, (None, None, hd), "q")
-    _shape(seq_len, (None,), "seq_len")
-    _shape(block_table, (seq_len.shape[0], None), "block_table")
-    T, Hq, _ = q.shape
-    R, kind = seq_len.shape[0], _KV_DTYPES[q.dtype]
-    qa, qs = _tokens(q, q.dtype, q.shape, "q", dev)
+    dtype, sh = q.dtype, q.shape
+    if dtype not in _KV_DTYPES:
+        raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
+    if len(sh) != 3 or sh[2] != hd:
+        raise ValueError(f"q must be [T, Hq, {hd}], got {tuple(sh)}")
+    T, Hq = sh[0], sh[1]
+    R, kind = _length(seq_len, "seq_len"), _KV_DTYPES[dtype]
+    qa, qs = _tokens(q, dtype, sh, "q", dev)
+    ta, cols = _table(block_table, R, dev)
     L = lib()
     if ws is None:
         # taken on the stream that uses it, so the allocator keeps it until the kernels are done
-        need = L.csa2_kv8_attn_workspace_size(Hq, Hk, hd, max_q, kind)
+        if torch.cuda.current_device() == dev:
+            need = L.csa2_kv8_attn_workspace_size(Hq, Hk, hd, max_q, kind)
+        else:  # it goes by the device's number of SMs
+            with torch.cuda.device(dev):
+                need = L.csa2_kv8_attn_workspace_size(Hq, Hk, hd, max_q, kind)
         if stream is None:
-            ws = workspace(need, dev)
+            ws = workspace(need, q.device)
         else:
             with torch.cuda.stream(stream):
-                ws = workspace(need, dev)
-    elif ws.dtype is not torch.uint8 or ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
+                ws = workspace(need, q.device)
+    elif ws.dtype is not _U8 or ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on cuda:{dev}")
     _check(_call_on(
-        dev, stream, L.csa2_kv8_attn, qa, qs, kind, T, Hq, Hk, hd, *cache, P, page,
-        _arg(block_table, torch.int32, block_table.shape, "block_table", dev), block_table.shape[1],
-        _arg(q_start, torch.int32, (R + 1,), "q_start", dev), _arg(seq_len, torch.int32, (R,), "seq_len", dev), R,
-        max_q, sm_scale, window, softcap, _arg(out, q.dtype, (T, Hq, hd), "out", dev),
-        None if lse is None else _arg(lse, torch.float32, (T, Hq), "lse", dev), ws.data_ptr(), ws.numel(),
+        dev, stream, L.csa2_kv8_attn, qa, qs, kind, T, Hq, Hk, hd, *cache, P, page, ta, cols,
+        _arg(q_start, _I32, (R + 1,), "q_start", dev), _arg(seq_len, _I32, (R,), "seq_len", dev), R,
+        max_q, sm_scale, window, softcap, _arg(out, dtype, (T, Hq, hd), "out", dev),
+        None if lse is None else _arg(lse, _F32, (T, Hq), "lse", dev), ws.data_ptr(), ws.numel(),
         _flag_arg(dev_status, dev)), "csa2_kv8_attn")

@@ -209,9 +209,9 @@ cudaError_t launch_paged_plan(const int32_t* ctx_len, const int32_t* new_len, in
 }
 
 // ------------------------------------------------------------------------------------
-// Release.  The valid pages of each released row are counted by one warp (the count goes to
-// every CTA of the cluster), scanned by every CTA, and written out by the same warps in row
-// order.
+// Release.  Every CTA scans the rows' page counts; the pages, laid end to end, are shared out
+// over the cluster's warps, read once to see that all are valid and once (from L1) to be
+// written at their place.  Only when one is not, valid pages are counted row by row instead.
 // ------------------------------------------------------------------------------------
 struct ReleaseArgs {
   const int32_t* seq_len;
@@ -227,11 +227,14 @@ struct ReleaseArgs {
   uint32_t* status;
 };
 
+constexpr int kMaxRanks = 8;
+
 __global__ void __launch_bounds__(kPlanThreads) paged_release_kernel(ReleaseArgs a) {
   __shared__ int64_t s_sums[32];
   __shared__ int32_t s_count[kPlanThreads];
-  __shared__ int64_t s_at[kPlanThreads];
+  __shared__ int64_t s_at[kPlanThreads];    // first page of each row, counted from the call's first
   __shared__ int32_t s_rows[kPlanThreads];  // pages of each released row of the chunk, else 0
+  __shared__ uint32_t s_bad[kMaxRanks];
   chain_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned rank = blockIdx.x, ranks = gridDim.x;  // one cluster
@@ -261,50 +264,94 @@ __global__ void __launch_bounds__(kPlanThreads) paged_release_kernel(ReleaseArgs
       }
     }
     s_rows[tid] = (int32_t)rows;
-    s_count[tid] = 0;
-    if (ranks > 1) cluster_sync_all();  // counts cleared everywhere; this chunk's inputs read
-    else __syncthreads();
+    int64_t total;
+    s_at[tid] = block_exclusive(rows, s_sums, &total);
+    __syncthreads();
     const int live = a.R - r0 < kPlanThreads ? a.R - r0 : kPlanThreads;
-    for (int i = rank * kPlanWarps + warp; i < live; i += ranks * kPlanWarps) {
-      const int m = s_rows[i];
-      if (m == 0) continue;
-      const int32_t* row = a.table + (int64_t)(r0 + i) * a.max_pages;
-      int cnt = 0;
-      for (int j = lane; j < m; j += 32) {
-        const int32_t id = row[j];
-        cnt += id >= 0 && id < a.n_pages;
+    // a warp takes consecutive pages, eight loads per lane at a time; `use` gets a page's place
+    const int64_t each = ((total + (int64_t)ranks * kPlanWarps - 1) / ((int64_t)ranks * kPlanWarps) + 31) & ~(int64_t)31;
+    const int64_t p_beg = (int64_t)(rank * kPlanWarps + warp) * each;
+    const int64_t p_end = p_beg + each < total ? p_beg + each : total;
+    const auto pages = [&](auto use) {
+      int i = p_beg < p_end ? last_at_most(s_at, live, p_beg) : 0;
+      for (int64_t p = p_beg + lane; p < p_end; p += 8 * 32) {
+        int32_t id[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int64_t q = p + x * 32;
+          id[x] = 0;
+          if (q < p_end) {
+            while (i + 1 < live && s_at[i + 1] <= q) ++i;
+            id[x] = a.table[(int64_t)(r0 + i) * a.max_pages + (q - s_at[i])];
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (p + x * 32 < p_end) use(p + x * 32, id[x]);
       }
-      cnt = __reduce_add_sync(0xffffffffu, cnt);
-      if (lane < ranks) {
-        if (ranks > 1) {
-          const uint32_t at = tc::mapa(tc::smem_u32(&s_count[i]), lane);
-          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(cnt) : "memory");
-        } else {
-          s_count[i] = cnt;
+    };
+    bool all = true;
+    pages([&](int64_t, int32_t id) { all &= id >= 0 && id < a.n_pages; });
+    uint32_t some = __syncthreads_or(!all);
+    if (ranks > 1) {
+      if (tid < ranks) {
+        const uint32_t at = tc::mapa(tc::smem_u32(&s_bad[rank]), tid);
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(some) : "memory");
+      }
+      cluster_sync_all();  // also: this chunk's inputs are read everywhere
+      some = 0;
+      for (unsigned k = 0; k < ranks; ++k) some |= s_bad[k];
+    }
+    if (!some) {
+      pages([&](int64_t p, int32_t id) {
+        const int64_t to = n_free + pushed + p;
+        if (to < a.free_cap) a.free_pages[to] = id;
+      });
+    } else {  // the valid pages of each row, counted by one warp for every CTA
+      bad |= CSA2_DEV_BAD_INDEX;
+      __syncthreads();
+      s_count[tid] = 0;
+      if (ranks > 1) cluster_sync_all();
+      else __syncthreads();
+      for (int i = rank * kPlanWarps + warp; i < live; i += ranks * kPlanWarps) {
+        const int m = s_rows[i];
+        if (m == 0) continue;
+        const int32_t* row = a.table + (int64_t)(r0 + i) * a.max_pages;
+        int cnt = 0;
+        for (int j = lane; j < m; j += 32) {
+          const int32_t id = row[j];
+          cnt += id >= 0 && id < a.n_pages;
+        }
+        cnt = __reduce_add_sync(0xffffffffu, cnt);
+        if (lane < ranks) {
+          if (ranks > 1) {
+            const uint32_t at = tc::mapa(tc::smem_u32(&s_count[i]), lane);
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(cnt) : "memory");
+          } else {
+            s_count[i] = cnt;
+          }
         }
       }
-      if (lane == 0 && cnt != m) bad |= CSA2_DEV_BAD_INDEX;
-    }
-    if (ranks > 1) cluster_sync_all();
-    else __syncthreads();
-    int64_t total;
-    s_at[tid] = n_free + pushed + block_exclusive(s_count[tid], s_sums, &total);
-    __syncthreads();
-    if (r < a.R && (unsigned)warp % ranks == rank) a.seq_len_out[r] = gone ? 0 : len;
-    for (int i = rank * kPlanWarps + warp; i < live; i += ranks * kPlanWarps) {
-      const int m = s_rows[i];
-      const int32_t* row = a.table + (int64_t)(r0 + i) * a.max_pages;
-      int64_t at = s_at[i];
-      for (int j0 = 0; j0 < m; j0 += 32) {
-        const int j = j0 + lane;
-        const int32_t id = j < m ? row[j] : -1;
-        const bool ok = id >= 0 && id < a.n_pages;
-        const unsigned mask = __ballot_sync(0xffffffffu, ok);
-        const int64_t to = at + __popc(mask & ((1u << lane) - 1u));
-        if (ok && to < a.free_cap) a.free_pages[to] = id;
-        at += __popc(mask);
+      if (ranks > 1) cluster_sync_all();
+      else __syncthreads();
+      s_at[tid] = n_free + pushed + block_exclusive(s_count[tid], s_sums, &total);
+      __syncthreads();
+      for (int i = rank * kPlanWarps + warp; i < live; i += ranks * kPlanWarps) {
+        const int m = s_rows[i];
+        const int32_t* row = a.table + (int64_t)(r0 + i) * a.max_pages;
+        int64_t at = s_at[i];
+        for (int j0 = 0; j0 < m; j0 += 32) {
+          const int j = j0 + lane;
+          const int32_t id = j < m ? row[j] : -1;
+          const bool ok = id >= 0 && id < a.n_pages;
+          const unsigned mask = __ballot_sync(0xffffffffu, ok);
+          const int64_t to = at + __popc(mask & ((1u << lane) - 1u));
+          if (ok && to < a.free_cap) a.free_pages[to] = id;
+          at += __popc(mask);
+        }
       }
     }
+    if (r < a.R && (unsigned)warp % ranks == rank) a.seq_len_out[r] = gone ? 0 : len;
     pushed += total;
     __syncthreads();
   }
@@ -326,7 +373,7 @@ cudaError_t launch_paged_release(const int32_t* seq_len, const int32_t* table, c
                                  uint32_t* status, cudaStream_t stream) {
   ReleaseArgs a{seq_len, table, release, R, log2_of(page), max_pages, free_pages, free_cap, n_free, n_pages,
                 seq_len_out, n_free_out, status};
-  const unsigned ranks = R > kPlanWarps ? 8 : 1;
+  const unsigned ranks = (int64_t)R * max_pages > 4 * kPlanThreads ? kMaxRanks : 1;
   cudaError_t e = launch_chained(paged_release_kernel, dim3(ranks), dim3(kPlanThreads), 0, stream, ranks, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -367,8 +414,25 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float s, float inv
                     e4m3x2_sat(y[4], y[5]) | (e4m3x2_sat(y[6], y[7]) << 16));
 }
 
+template <typename T>
+struct PairOf;
+template <>
+struct PairOf<__nv_bfloat16> { using type = __nv_bfloat162; };
+template <>
+struct PairOf<__half> { using type = __half2; };
+template <typename T>
+using Pair = typename PairOf<T>::type;
+template <typename T>
+__device__ __forceinline__ Pair<T> zero_pair() {
+  Pair<T> z;
+  *reinterpret_cast<uint32_t*>(&z) = 0;
+  return z;
+}
+__device__ __forceinline__ float larger(__nv_bfloat162 v) { return fmaxf(__low2float(v), __high2float(v)); }
+__device__ __forceinline__ float larger(__half2 v) { return fmaxf(__low2float(v), __high2float(v)); }
+
 template <int HD, typename T, int GW>
-__global__ void __launch_bounds__(256) kv8_append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(256, 4) kv8_append_kernel(AppendArgs a) {
   constexpr int kPage = GW * 16, kUnits = 8 / GW;
   constexpr int kLanes = HD / 8;         // lanes per row
   constexpr int kRowsAt = 32 / kLanes;   // rows per warp load
@@ -380,97 +444,106 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(AppendArgs a) {
   const int64_t u = (int64_t)blockIdx.x * kUnits + unit;
   const int h = (int)(u % a.Hk);
   const int kv = blockIdx.y;
+  const uint8_t* x_all = kv ? a.x[1] : a.x[0];
+  const int64_t stride = kv ? a.stride[1] : a.stride[0];
+  uint8_t* cache = kv ? a.cache[1] : a.cache[0];
+  float* scale = kv ? a.scale[1] : a.scale[0];
   const int64_t w0 = u / a.Hk * a.win;
   const int64_t w1 = w0 + a.win < a.T ? w0 + a.win : a.T;
   const int64_t n_slots = a.n_pages * kPage;
   uint32_t bad = 0;
-  for (int64_t t = w0; t < w1; ++t) {  // the same for every warp of the unit
-    const int64_t slot = a.slot[t];
-    if (slot < 0 || slot >= n_slots) {
-      if (slot != -1) bad = CSA2_DEV_BAD_INDEX;
-      continue;
-    }
-    if (t > 0) {
-      const int64_t prev = a.slot[t - 1];
-      if (prev >= 0 && prev < n_slots && prev / kPage == slot / kPage) {
-        if (prev + 1 != slot) bad = CSA2_DEV_BAD_INDEX;
-        continue;  // not the first of its page
+  for (int64_t t0 = w0; t0 < w1; t0 += 32) {  // the same for every warp of the unit
+    int64_t slots = -1;
+    bool first = false;  // this lane's token is the first of its page
+    if (t0 + lane < w1) {
+      slots = a.slot[t0 + lane];
+      const int64_t prev = t0 + lane > 0 ? a.slot[t0 + lane - 1] : -1;
+      if (slots < 0 || slots >= n_slots) {
+        if (slots != -1) bad = CSA2_DEV_BAD_INDEX;
+      } else if (prev >= 0 && prev < n_slots && prev / kPage == slots / kPage) {
+        if (prev + 1 != slots) bad = CSA2_DEV_BAD_INDEX;
+      } else {
+        first = true;
       }
     }
-    const int64_t pid = slot / kPage;
-    const int off = (int)(slot % kPage);
-    int n = 1;  // tokens of this page: consecutive slots
-    {
-      const int most = kPage - off;
+    for (unsigned todo = __ballot_sync(0xffffffffu, first); todo; todo &= todo - 1) {
+      const int from = __ffs(todo) - 1;
+      const int64_t t = t0 + from, slot = __shfl_sync(0xffffffffu, slots, from);
+      const int64_t pid = slot / kPage;
+      const int off = (int)(slot % kPage);
+      int n = 1;  // tokens of this page: consecutive slots
+      {
+        const int most = kPage - off;
 #pragma unroll
-      for (int i0 = 0; i0 < kPage; i0 += 32) {
-        const int i = i0 + lane;
-        const bool in = i < most && t + i < a.T && a.slot[t + i] == slot + i;
-        const unsigned m = __ballot_sync(0xffffffffu, in);
-        if (n >= i0) n = i0 + (m == 0xffffffffu ? 32 : __ffs(~m) - 1);
-        if (m != 0xffffffffu) break;
+        for (int i0 = 0; i0 < kPage; i0 += 32) {
+          const int i = i0 + lane;
+          const bool in = i < most && t + i < a.T && a.slot[t + i] == slot + i;
+          const unsigned m = __ballot_sync(0xffffffffu, in);
+          if (n >= i0) n = i0 + (m == 0xffffffffu ? 32 : __ffs(~m) - 1);
+          if (m != 0xffffffffu) break;
+        }
       }
-    }
-    float* sp = a.scale[kv] + pid * a.Hk + h;
-    const float s_old = off > 0 ? *sp : 0.0f;
-    const uint8_t* x0 = a.x[kv] + t * a.stride[kv] + (int64_t)h * (HD * 2) + (lane % kLanes) * 16;
-    uint4 raw[kLoads];
-    float amax = 0.0f;
+      float* sp = scale + pid * a.Hk + h;
+      const float s_old = off > 0 ? *sp : 0.0f;
+      const uint8_t* x0 = x_all + t * stride + (int64_t)h * (HD * 2) + (lane % kLanes) * 16;
+      uint4 raw[kLoads];
 #pragma unroll
-    for (int k = 0; k < kLoads; ++k) {
-      const int i = g * 16 + k * kRowsAt + lane / kLanes - off;  // token of the run
-      raw[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (i >= 0 && i < n) raw[k] = __ldcs(reinterpret_cast<const uint4*>(x0 + i * a.stride[kv]));
-    }
+      for (int k = 0; k < kLoads; ++k) {
+        const int i = g * 16 + k * kRowsAt + lane / kLanes - off;  // token of the run
+        raw[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (i >= 0 && i < n) raw[k] = __ldcs(reinterpret_cast<const uint4*>(x0 + i * stride));
+      }
+      Pair<T> top = zero_pair<T>();  // largest magnitudes so far; NaN counts for nothing
 #pragma unroll
-    for (int k = 0; k < kLoads; ++k) {
-      float x[8];
-      unpack8<T>(raw[k], x);
+      for (int k = 0; k < kLoads; ++k) {
+        const uint32_t v[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
-    }
-    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));  // >= 0: ordered as integers
-    if (GW > 1) {
-      if (lane == 0) s_amax[warp] = amax;
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + unit), "n"(GW * 32) : "memory");
+        for (int i = 0; i < 4; ++i) top = __hmax2(top, __habs2(*reinterpret_cast<const Pair<T>*>(&v[i])));
+      }
+      float amax = larger(top);
+      amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));  // >= 0: ordered as integers
+      if (GW > 1) {
+        if (lane == 0) s_amax[warp] = amax;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + unit), "n"(GW * 32) : "memory");
 #pragma unroll
-      for (int i = 0; i < GW; ++i) amax = fmaxf(amax, s_amax[unit * GW + i]);
-    }
-    const float s = fmaxf(block_scale(amax), s_old);
-    const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0;
-    const float inv = __fdiv_rn(1.0f, s);
-    uint8_t* c0 = a.cache[kv] + (pid * a.Hk + h) * (int64_t)(kPage * HD) + (lane % kLanes) * 8;
-    if (off > 0 && s != s_old) {  // earlier rows under the larger scale
-      const float ratio = __fdiv_rn(s_old, s);
+        for (int i = 0; i < GW; ++i) amax = fmaxf(amax, s_amax[unit * GW + i]);
+      }
+      const float s = fmaxf(block_scale(amax), s_old);
+      const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0;
+      const float inv = __fdiv_rn(1.0f, s);
+      uint8_t* c0 = cache + (pid * a.Hk + h) * (int64_t)(kPage * HD) + (lane % kLanes) * 8;
+      if (off > 0 && s != s_old) {  // earlier rows under the larger scale
+        const float ratio = __fdiv_rn(s_old, s);
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+          const int row = g * 16 + k * kRowsAt + lane / kLanes;
+          if (row < off) {
+            uint2* p = reinterpret_cast<uint2*>(c0 + row * HD);
+            const uint2 c = *p;
+            float x[8];
+            e4m3x4_f32(c.x, x);
+            e4m3x4_f32(c.y, x + 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] *= ratio;
+            *p = encode8(x, 1.0f, 1.0f, true);
+          }
+        }
+      }
 #pragma unroll
       for (int k = 0; k < kLoads; ++k) {
         const int row = g * 16 + k * kRowsAt + lane / kLanes;
-        if (row < off) {
-          uint2* p = reinterpret_cast<uint2*>(c0 + row * HD);
-          const uint2 c = *p;
+        if (row >= off && row < off + n) {
           float x[8];
-          e4m3x4_f32(c.x, x);
-          e4m3x4_f32(c.y, x + 4);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] *= ratio;
-          *p = encode8(x, 1.0f, 1.0f, true);
+          unpack8<T>(raw[k], x);
+          *reinterpret_cast<uint2*>(c0 + row * HD) = encode8(x, s, inv, pow2);
         }
       }
+      if (g == 0 && lane == 0) *sp = s;
+      if (GW > 1)  // s_amax is free again
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + unit), "n"(GW * 32) : "memory");
     }
-#pragma unroll
-    for (int k = 0; k < kLoads; ++k) {
-      const int row = g * 16 + k * kRowsAt + lane / kLanes;
-      if (row >= off && row < off + n) {
-        float x[8];
-        unpack8<T>(raw[k], x);
-        *reinterpret_cast<uint2*>(c0 + row * HD) = encode8(x, s, inv, pow2);
-      }
-    }
-    if (g == 0 && lane == 0) *sp = s;
-    if (GW > 1)  // s_amax is free again
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + unit), "n"(GW * 32) : "memory");
   }
-  if (bad && h == 0 && kv == 0 && g == 0 && lane == 0) flag(a.status, bad);
+  if (bad && h == 0 && kv == 0 && g == 0) flag(a.status, bad);
 }
 
 template <int HD, typename T>

@@ -357,8 +357,7 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
   const int c0 = wg * CW;
   const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
   const float cap2 = C::CAP ? a.softcap * kLog2e : 0.0f;
-  int32_t* meta = a.meta + (int64_t)blockIdx.x * kMetaInts;
-  if (tid < 2) meta[tid] = 0;
+  if (tid == 0) a.meta[(int64_t)blockIdx.x * kMetaInts] = 0;
   bool bad = false;
   int64_t n = 0;
   Walk w;
@@ -569,16 +568,7 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
       }
     }
     tc::fence_before_sync();
-    if (!whole && tid == 0) {
-      if (w.first) {
-        meta[1] = 1;
-        meta[2] = w.r;
-        meta[3] = w.hh;
-        meta[4] = w.qb;
-      } else {
-        meta[0] = w.last ? 2 : 1;
-      }
-    }
+    if (!whole && w.first && tid == 0) note_item(a, sh.share, w);
     // the next piece's queries may replace these: every product of this one has completed, and
     // every softmax thread has read its columns
     asm volatile("bar.sync 3, %0;" ::"n"(C::kSoft) : "memory");
@@ -693,7 +683,7 @@ static cudaError_t launch_kv8_t(const CUtensorMap& km, const CUtensorMap& vm, Kv
   if (e != cudaSuccess) return e;
   e = launch_chained(kv8_attn_kernel<C, T>, dim3(ctas), dim3(C::kThreads), C::kSmem, stream, 0, km, vm, a);
   if (e != cudaSuccess) return e;
-  e = launch_chained(kv8_merge_kernel<C::NC, C::kHD, T>, dim3(ctas, C::NC / 8), dim3(C::kHD), 0, stream, 0, a, ctas, kLift);
+  e = launch_chained(kv8_merge_kernel<C::NC, C::kHD, T>, dim3(ctas, C::NC / 8), dim3(C::kHD * kMergeSplit), 0, stream, 0, a, kLift);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

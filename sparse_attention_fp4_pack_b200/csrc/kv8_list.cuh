@@ -43,8 +43,9 @@ struct KvAttnArgs {
 };
 
 // Partial results of CTA c: slot 0 the piece that continues an item, slot 1 the one that
-// starts an item and does not end it.  meta: [0] slot 0 (0 none, 1 goes on, 2 ends the item),
-// [1] slot 1 used, [2..5] its request, head, head block, query block.
+// starts an item and does not end it.  meta: [0] slot 1 is used; then [1] the CTA whose slot 0
+// ends the item, [2] key head * head blocks + head block, [3] query block, [4] first row and
+// [5] number of queries of the request.
 constexpr int kMetaInts = 8;
 
 // Rows of hd bytes from `row` on (a box of the map) into shared memory.
@@ -157,6 +158,7 @@ __device__ __forceinline__ int64_t lane_row_tiles(const KvAttnArgs& a, const Sha
 // This CTA's share of the list: its length, and where it begins.
 struct Share {
   int64_t left;
+  int64_t t0, total;   // first tile of the share, tiles of the list
   int r, hh, qb, off;  // request, key head * nhb + head block, query block, tile inside the item
 };
 
@@ -212,6 +214,26 @@ struct Walk {
   }
 };
 
+// First tile of CTA c's share.  With fewer tiles than CTAs the first CTAs take one each, so the
+// pieces of an item are always neighbours.
+__device__ __forceinline__ int64_t share_start(int64_t total, int64_t c) {
+  const int64_t C = total < gridDim.x ? (total > 0 ? total : 1) : gridDim.x;
+  return c < C ? total / C * c + total % C * c / C : total;
+}
+// Notes the item that this CTA starts with `w` and does not end.
+__device__ __forceinline__ void note_item(const KvAttnArgs& a, const Share& share, const Walk& w) {
+  const int64_t last = share_start(share.total, blockIdx.x + 1) + (w.g.tiles - w.off - w.take) - 1;  // its last tile
+  int c = blockIdx.x + 1;
+  while (share_start(share.total, c + 1) <= last) ++c;
+  int32_t* meta = a.meta + (int64_t)blockIdx.x * kMetaInts;
+  meta[0] = 1;
+  meta[1] = c;
+  meta[2] = w.hh;
+  meta[3] = w.qb;
+  meta[4] = w.x.q0;
+  meta[5] = w.x.n;
+}
+
 // Computed by the whole CTA (kThreads threads); `sums` holds a value per thread.
 template <int kThreads>
 __device__ void find_share(const KvAttnArgs& a, const Shape& s, int64_t* sums, Share* out, uint32_t* bad) {
@@ -237,9 +259,8 @@ __device__ void find_share(const KvAttnArgs& a, const Shape& s, int64_t* sums, S
       if (lane >= o) upto += y;
     }
     const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
-    const int64_t c = blockIdx.x, C = gridDim.x;
-    const int64_t t0 = total / C * c + total % C * c / C, t1 = total / C * (c + 1) + total % C * (c + 1) / C;
-    Share w = {t1 - t0, 0, 0, 0, 0};
+    const int64_t t0 = share_start(total, blockIdx.x), t1 = share_start(total, blockIdx.x + 1);
+    Share w = {t1 - t0, t0, total, 0, 0, 0, 0};
     if (w.left > 0) {
       // the thread whose requests hold tile t0 ...
       const unsigned m = __ballot_sync(0xffffffffu, upto > t0);
@@ -327,47 +348,46 @@ __device__ __forceinline__ bool kv_wait(int* abort, uint64_t& bar, uint32_t pari
 
 // Joins the pieces of the item that CTA blockIdx.x starts and does not end: with M the largest
 // of the pieces' maxima, out = sum 2^(m - M) O / sum 2^(m - M) l.  blockIdx.y: 8 columns; a
-// thread one channel of them.  The pieces' count and weights come first (a lane per piece), so
-// the sums over the pieces are independent loads.
+// thread one channel of them, kMergeSplit threads per channel take the pieces in turn.  The pieces'
+// weights come first (a lane per piece), so the loads of the sums do not wait for one another.
+constexpr int kMergeSplit = 4;
+
 template <int NC, int HD, typename T>
-__global__ void __launch_bounds__(HD) kv8_merge_kernel(const KvAttnArgs a, int ctas, float lift) {
-  constexpr int kChunk = 64, kPart = NC * (HD + 2), kWarps = HD / 32;
-  __shared__ int s_end;
+__global__ void __launch_bounds__(HD* kMergeSplit) kv8_merge_kernel(const KvAttnArgs a, float lift) {
+  constexpr int kChunk = 64, kPart = NC * (HD + 2), kThreads = HD * kMergeSplit, kWarps = kThreads / 32;
   __shared__ float s_w[kChunk][8], s_m[8], s_l[8];
+  __shared__ float s_acc[kMergeSplit - 1][8][HD];
   chain_enter();
-  const int cta = blockIdx.x, c0 = blockIdx.y * 8, d = threadIdx.x, lane = d & 31, warp = d >> 5;
-  const int32_t* meta = a.meta + (int64_t)cta * kMetaInts;
-  if (meta[1] == 0) return;
-  if (d == 0) s_end = ctas;
-  __syncthreads();
-  for (int base = cta + 1; base < ctas; base += HD) {  // the piece that ends the item
-    const int k = base + d;
-    if (k < ctas && a.meta[(int64_t)k * kMetaInts] == 2) atomicMin(&s_end, k);
-    __syncthreads();
-    if (s_end < ctas) break;
-  }
-  const int n = (s_end < ctas ? s_end + 1 : ctas) - cta;  // piece i is CTA cta + i's
-  const auto piece = [&](int i) { return a.part + ((int64_t)(cta + i) * 2 + (i == 0 ? 1 : 0)) * kPart; };
-  const auto stats = [&](int i, int j) {  // maximum and sum; (0, 0) of a CTA without work
-    if (i > 0 && a.meta[(int64_t)(cta + i) * kMetaInts] == 0) return make_float2(0.0f, 0.0f);
-    return *reinterpret_cast<const float2*>(piece(i) + NC * HD + 2 * (c0 + j));
-  };
+  const int cta = blockIdx.x, c0 = blockIdx.y * 8;
+  const int tid = threadIdx.x, d = tid % HD, split = tid / HD, lane = tid & 31, warp = tid >> 5;
+  const int4 m0 = *reinterpret_cast<const int4*>(a.meta + (int64_t)cta * kMetaInts);
+  const int2 m1 = *reinterpret_cast<const int2*>(a.meta + (int64_t)cta * kMetaInts + 4);
+  if (m0.x == 0) return;
+  const Shape s = shape_of<NC>(a);
+  const int hh = m0.z, qb = m0.w, q0 = m1.x, nq = m1.y, hb = hh % s.nhb;
+  if (qb * s.QB + c0 / s.HB >= nq) return;  // no query in these columns
+  const int n = m0.y + 1 - cta;             // piece i is CTA cta + i's
+  const float* part = a.part + (int64_t)cta * 2 * kPart;
+  const auto piece = [&](int i) { return part + (i == 0 ? kPart : (int64_t)i * 2 * kPart); };
+  const auto stats = [&](int i, int j) { return *reinterpret_cast<const float2*>(piece(i) + NC * HD + 2 * (c0 + j)); };
   for (int j = warp; j < 8; j += kWarps) {
     float M = -INFINITY, l = 0.0f;
     for (int i = lane; i < n; i += 32) {
-      const float2 s = stats(i, j);
-      if (s.y != 0.0f) M = fmaxf(M, s.x);  // a piece that saw no key has no maximum
+      const float2 v = stats(i, j);
+      if (v.y != 0.0f) {  // a piece that saw no key has no maximum
+        const float top = fmaxf(M, v.x);
+        l = l * exp2f(M - top) + v.y * exp2f(v.x - top);
+        M = top;
+      }
     }
+    float top = M;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    for (int i = lane; i < n; i += 32) {
-      const float2 s = stats(i, j);
-      if (s.y != 0.0f) l += s.y * exp2f(s.x - M);
-    }
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    l = l != 0.0f ? l * exp2f(M - top) : 0.0f;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
-      s_m[j] = M;
+      s_m[j] = top;
       s_l[j] = l;
     }
   }
@@ -377,32 +397,40 @@ __global__ void __launch_bounds__(HD) kv8_merge_kernel(const KvAttnArgs a, int c
   for (int i0 = 0; i0 < n; i0 += kChunk) {
     const int in = n - i0 < kChunk ? n - i0 : kChunk;
     __syncthreads();
-    for (int x = d; x < in * 8; x += HD) {
-      const float2 s = stats(i0 + x / 8, x % 8);
-      s_w[x / 8][x % 8] = s.y != 0.0f ? exp2f(s.x - s_m[x % 8]) : 0.0f;
+    for (int k = tid; k < in * 8; k += kThreads) {
+      const float2 v = stats(i0 + k / 8, k % 8);
+      s_w[k / 8][k % 8] = v.y != 0.0f ? exp2f(v.x - s_m[k % 8]) : 0.0f;
     }
     __syncthreads();
 #pragma unroll 4
-    for (int i = 0; i < in; ++i) {
+    for (int i = split; i < in; i += kMergeSplit) {
       const float* p = piece(i0 + i) + c0 * HD + d;
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = p[j * HD];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float w = s_w[i][j];
-        if (w != 0.0f) acc[j] = fmaf(p[j * HD], w, acc[j]);  // what holds nothing was not written
+        acc[j] = w != 0.0f ? fmaf(o[j], w, acc[j]) : acc[j];  // columns without a row hold any bits
       }
     }
   }
-  const Shape s = shape_of<NC>(a);
-  const int r = meta[2], hh = meta[3], qb = meta[4], hb = hh % s.nhb;
-  uint32_t bad = 0;
-  const Request x = request_of(a, s, r, &bad);
+  if (split > 0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s_acc[split - 1][j][d] = acc[j];
+  }
+  __syncthreads();
+  if (split > 0) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int c = c0 + j, qi = c / s.HB, hd = c - qi * s.HB, i = qb * s.QB + qi;
-    if (qi >= s.QB || i >= x.n || hd >= s.G - hb * s.HB) continue;
-    const int64_t to = (int64_t)(x.q0 + i) * a.Hq + hh / s.nhb * s.G + hb * s.HB + hd;
+    if (qi >= s.QB || i >= nq || hd >= s.G - hb * s.HB) continue;
+    const int64_t to = (int64_t)(q0 + i) * a.Hq + hh / s.nhb * s.G + hb * s.HB + hd;
     const float l = s_l[j];
-    reinterpret_cast<T*>(a.out)[to * HD + d] = from_float<T>(l != 0.0f ? __fdiv_rn(acc[j], l) : 0.0f);
+    float o = acc[j];
+#pragma unroll
+    for (int k = 0; k < kMergeSplit - 1; ++k) o += s_acc[k][j][d];
+    reinterpret_cast<T*>(a.out)[to * HD + d] = from_float<T>(l != 0.0f ? __fdiv_rn(o, l) : 0.0f);
     if (a.lse && d == 0) a.lse[to] = l != 0.0f ? (s_m[j] + log2f(l) - lift) * kLn2 : -INFINITY;
   }
 }

@@ -334,8 +334,7 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
   const uint32_t s_at = lanes + g * 128, o_at = lanes + C::kColO + g * C::kHD;
   float2* joint = reinterpret_cast<float2*>(smem_p + C::kOffQ + C::kTile);  // slot 1's rows are unused then
   const float cap2 = C::CAP ? a.softcap * kLog2e : 0.0f;
-  int32_t* meta = a.meta + (int64_t)blockIdx.x * kMetaInts;
-  if (tid < 2) meta[tid] = 0;
+  if (tid == 0) a.meta[(int64_t)blockIdx.x * kMetaInts] = 0;
   bool bad = false;
   uint32_t n_s = 0, tile0 = 0, piece = 0;  // this slot's tiles; K tiles and pieces before this piece
   Walk w = {};
@@ -539,16 +538,7 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
           for (int z = 0; z < 4; ++z) out[z] = make_float4(x[4 * z], x[4 * z + 1], x[4 * z + 2], x[4 * z + 3]);
         }
       }
-      if (!whole && tid == 0) {
-        if (w.first) {
-          meta[1] = 1;
-          meta[2] = w.r;
-          meta[3] = w.hh;
-          meta[4] = w.qb;
-        } else {
-          meta[0] = w.last ? 2 : 1;
-        }
-      }
+      if (!whole && w.first && tid == 0) note_item(a, sh.share, w);
     }
     tc::fence_before_sync();
     if (shared_rows)  // slot 1's output has been read, the next piece may overwrite it
@@ -632,8 +622,8 @@ static cudaError_t launch_wide_t(KvAttnArgs a, const CUtensorMap& km, const CUte
   if (e != cudaSuccess) return e;
   e = launch_chained(kv8_wide_kernel<C, T>, dim3(num_sms), dim3(C::kThreads), C::kSmem, stream, 0, km, vm, a);
   if (e != cudaSuccess) return e;
-  e = launch_chained(kv8_merge_kernel<C::NC, C::kHD, T>, dim3(num_sms, C::NC / 8), dim3(C::kHD), 0, stream, 0, a, num_sms,
-                     kWideLift);
+  e = launch_chained(kv8_merge_kernel<C::NC, C::kHD, T>, dim3(num_sms, C::NC / 8), dim3(C::kHD * kMergeSplit), 0,
+                     stream, 0, a, kWideLift);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
