@@ -71,13 +71,6 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool 
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
-}
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
   if constexpr (N == 8) tc::tmem_ld8(addr, r);
@@ -215,7 +208,7 @@ __device__ void produce(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, ui
   if (bad) flag(a.status, bad);
 }
 
-// ---- products (one thread) -------------------------------------------------------------
+// ---- products (one warp) ----------------------------------------------------------------
 template <class C>
 __device__ void multiply(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uint32_t smem, uint32_t tmem) {
   constexpr uint32_t kIdS = idesc_e4m3(kKeys, C::NS, false, false);
@@ -229,44 +222,45 @@ __device__ void multiply(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, u
   const uint64_t dp = tc::smem_desc(smem + C::kOffP, 128, 16 * kKeys, 0);
   int64_t n = 0;
   uint32_t piece = 0;
+  const bool on = (threadIdx.x & 31) == 0;
   bool ok = true;
   Walk w;
   auto scores = [&](int64_t m) {  // S of tile m
     const int st = (int)(m % C::kStages);
-    ok = kv_wait(&sh.abort, sh.kfull[st], (uint32_t)(m / C::kStages) & 1u) &&
-         kv_wait(&sh.abort, sh.sfree[m & 1], ((uint32_t)(m >> 1) & 1u) ^ 1u);
+    ok = kv_wait_all(sh, sh.kfull[st], (uint32_t)(m / C::kStages) & 1u) &&
+         kv_wait_all(sh, sh.sfree[m & 1], ((uint32_t)(m >> 1) & 1u) ^ 1u);
     if (!ok) return;
     tc::fence_after_sync();
     const uint64_t dk = tc::desc_add(dk0, st * C::kTile);
     const uint32_t d = tmem + C::kColS + (uint32_t)(m & 1) * C::NS;
 #pragma unroll
     for (int k = 0; k < C::kHD / 32; ++k)
-      mma_e4m3(d, tc::desc_add(dk, 32 * k), tc::desc_add(dq, 32 * k), kIdS, k > 0);
-    tc::commit(tc::smem_u32(&sh.sfull[m & 1]));
-    tc::commit(tc::smem_u32(&sh.kempty[st]));
+      mma_e4m3(on, d, tc::desc_add(dk, 32 * k), tc::desc_add(dq, 32 * k), kIdS, k > 0);
+    commit_if(on, tc::smem_u32(&sh.sfull[m & 1]));
+    commit_if(on, tc::smem_u32(&sh.kempty[st]));
   };
   for (w.start(a, s, sh.share); ok && w.left > 0; w.next(a, s), ++piece) {
-    ok = kv_wait(&sh.abort, sh.qfull, piece & 1u);
+    ok = kv_wait_all(sh, sh.qfull, piece & 1u);
     if (!ok) break;
     scores(n);
     for (int i = 0; ok && i < w.take; ++i, ++n) {
       if (i + 1 < w.take) scores(n + 1);
       const int st = (int)(n % C::kStages);
-      ok = ok && kv_wait(&sh.abort, sh.vfull[st], (uint32_t)(n / C::kStages) & 1u) &&
-           kv_wait(&sh.abort, sh.pfull, (uint32_t)n & 1u);
+      ok = ok && kv_wait_all(sh, sh.vfull[st], (uint32_t)(n / C::kStages) & 1u) &&
+           kv_wait_all(sh, sh.pfull, (uint32_t)n & 1u);
       if (!ok) break;
       tc::fence_after_sync();
       const uint64_t dv = tc::desc_add(dv0, st * C::kTile);
 #pragma unroll
       for (int k = 0; k < kKeys / 32; ++k)
-        mma_e4m3(tmem + C::kColO, tc::desc_add(dv, 32 * k * C::kHD), tc::desc_add(dp, 32 * k * 16), kIdO,
+        mma_e4m3(on, tmem + C::kColO, tc::desc_add(dv, 32 * k * C::kHD), tc::desc_add(dp, 32 * k * 16), kIdO,
                  i > 0 || k > 0);
-      tc::commit(tc::smem_u32(&sh.vempty[st]));
-      tc::commit(tc::smem_u32(&sh.pvdone));
+      commit_if(on, tc::smem_u32(&sh.vempty[st]));
+      commit_if(on, tc::smem_u32(&sh.pvdone));
     }
   }
   if (!ok) {  // given up: no product may run after the tensor memory is freed
-    tc::commit(tc::smem_u32(&sh.drain));
+    commit_if(on, tc::smem_u32(&sh.drain));
     tc::mbar_wait(tc::smem_u32(&sh.drain), 0, kKvPolls);
   }
 }
@@ -582,7 +576,7 @@ __global__ void __launch_bounds__(C::kThreads) kv8_attn_kernel(const __grid_cons
   extern __shared__ uint8_t raw[];
   __shared__ KvShared<C> sh;
   uint8_t* smem = tc::align_smem_1024(raw);
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5);
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       tc::mbar_init(tc::smem_u32(&sh.kfull[i]), 1);
@@ -613,12 +607,12 @@ __global__ void __launch_bounds__(C::kThreads) kv8_attn_kernel(const __grid_cons
   __syncthreads();
   tc::fence_after_sync();
   chain_launch_dependents();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = uniform(sh.tmem);
   if (warp < C::kSoft / 32) {
     soften<C, T>(a, s, sh, smem, tmem);
   } else if (warp == C::kSoft / 32) {
     produce<C>(a, s, sh, tc::smem_u32(smem), &kmap, &vmap);
-  } else if ((tid & 31) == 0) {
+  } else {
     multiply<C>(a, s, sh, tc::smem_u32(smem), tmem);
   }
   __syncwarp();
@@ -683,7 +677,7 @@ static cudaError_t launch_kv8_t(const CUtensorMap& km, const CUtensorMap& vm, Kv
   if (e != cudaSuccess) return e;
   e = launch_chained(kv8_attn_kernel<C, T>, dim3(ctas), dim3(C::kThreads), C::kSmem, stream, 0, km, vm, a);
   if (e != cudaSuccess) return e;
-  e = launch_chained(kv8_merge_kernel<C::NC, C::kHD, T>, dim3(ctas, C::NC / 8), dim3(C::kHD * kMergeSplit), 0, stream, 0, a, kLift);
+  e = launch_chained(kv8_merge_kernel<C::NC, C::kHD, T>, dim3(ctas, C::NC / 8), dim3(kMergeThreads), 0, stream, 0, a, kLift);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -56,6 +56,75 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
       "l"(map), "r"(0), "r"(row), "r"(bar)
       : "memory");
 }
+// Bounded wait that also ends when another role of the CTA has given up (*abort != 0).
+__device__ __forceinline__ bool kv_wait(int* abort, uint64_t& bar, uint32_t parity) {
+  const uint32_t b = tc::smem_u32(&bar);
+  uint64_t t0 = 0;
+  for (uint32_t i = 0; i < kKvPolls; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(b), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 63u) == 63u) {
+      if (*reinterpret_cast<volatile int*>(abort)) return false;
+      const uint64_t now = tc::globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > tc::kWaitLimitNs) break;
+    }
+  }
+  *reinterpret_cast<volatile int*>(abort) = 1;
+  return false;
+}
+
+// Lane 0's value, known to be the same in the whole warp.
+template <typename T>
+__device__ __forceinline__ T uniform(T x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Products and their completion, issued by the lane where `on` holds.  The whole warp runs the
+// issuing loop: descriptors then stay in uniform registers, where a lone thread's would be
+// moved there one by one before every product.
+__device__ __forceinline__ void mma_ss(bool on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"((uint32_t)on));
+}
+__device__ __forceinline__ void mma_ts(bool on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"((uint32_t)on));
+}
+__device__ __forceinline__ void mma_e4m3(bool on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"((uint32_t)on));
+}
+__device__ __forceinline__ void commit_if(bool on, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"((uint32_t)on)
+      : "memory");
+}
+// kv_wait of a whole warp.
+template <class Sh>
+__device__ __forceinline__ bool kv_wait_all(Sh& sh, uint64_t& bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, kv_wait(&sh.abort, bar, parity));
+}
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -216,15 +285,16 @@ struct Walk {
 
 // First tile of CTA c's share.  With fewer tiles than CTAs the first CTAs take one each, so the
 // pieces of an item are always neighbours.
+__device__ __forceinline__ int64_t share_ctas(int64_t total) { return total < gridDim.x ? total : gridDim.x; }
 __device__ __forceinline__ int64_t share_start(int64_t total, int64_t c) {
-  const int64_t C = total < gridDim.x ? (total > 0 ? total : 1) : gridDim.x;
-  return c < C ? total / C * c + total % C * c / C : total;
+  const int64_t C = share_ctas(total);
+  return c < C ? total * c / C : total;  // at most 2^31 items of 2^23 tiles: below 2^63
 }
 // Notes the item that this CTA starts with `w` and does not end.
 __device__ __forceinline__ void note_item(const KvAttnArgs& a, const Share& share, const Walk& w) {
   const int64_t last = share_start(share.total, blockIdx.x + 1) + (w.g.tiles - w.off - w.take) - 1;  // its last tile
-  int c = blockIdx.x + 1;
-  while (share_start(share.total, c + 1) <= last) ++c;
+  // the largest c with total * c / C <= last
+  const int c = (int)(((last + 1) * share_ctas(share.total) - 1) / share.total);
   int32_t* meta = a.meta + (int64_t)blockIdx.x * kMetaInts;
   meta[0] = 1;
   meta[1] = c;
@@ -321,118 +391,63 @@ __device__ void find_share(const KvAttnArgs& a, const Shape& s, int64_t* sums, S
   __syncthreads();
 }
 
-// Bounded wait that also ends when another role of the CTA has given up (*abort != 0).
-__device__ __forceinline__ bool kv_wait(int* abort, uint64_t& bar, uint32_t parity) {
-  const uint32_t b = tc::smem_u32(&bar);
-  uint64_t t0 = 0;
-  for (uint32_t i = 0; i < kKvPolls; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(b), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((i & 63u) == 63u) {
-      if (*reinterpret_cast<volatile int*>(abort)) return false;
-      const uint64_t now = tc::globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      else if (now - t0 > tc::kWaitLimitNs) break;
-    }
-  }
-  *reinterpret_cast<volatile int*>(abort) = 1;
-  return false;
-}
 
 // Joins the pieces of the item that CTA blockIdx.x starts and does not end: with M the largest
-// of the pieces' maxima, out = sum 2^(m - M) O / sum 2^(m - M) l.  blockIdx.y: 8 columns; a
-// thread one channel of them, kMergeSplit threads per channel take the pieces in turn.  The pieces'
-// weights come first (a lane per piece), so the loads of the sums do not wait for one another.
-constexpr int kMergeSplit = 4;
+// of the pieces' maxima, out = sum 2^(m - M) O / sum 2^(m - M) l.  A warp joins one column: its
+// lanes first hold the statistics of 32 pieces, then 4 (2 of 64) channels each, so the loads of
+// all pieces are independent.
+constexpr int kMergeThreads = 256;  // 8 columns
 
 template <int NC, int HD, typename T>
-__global__ void __launch_bounds__(HD* kMergeSplit) kv8_merge_kernel(const KvAttnArgs a, float lift) {
-  constexpr int kChunk = 64, kPart = NC * (HD + 2), kThreads = HD * kMergeSplit, kWarps = kThreads / 32;
-  __shared__ float s_w[kChunk][8], s_m[8], s_l[8];
-  __shared__ float s_acc[kMergeSplit - 1][8][HD];
+__global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const KvAttnArgs a, float lift) {
+  constexpr int kPart = NC * (HD + 2), kPer = HD / 32;
+  using Vec = std::conditional_t<kPer == 4, float4, float2>;
   chain_enter();
-  const int cta = blockIdx.x, c0 = blockIdx.y * 8;
-  const int tid = threadIdx.x, d = tid % HD, split = tid / HD, lane = tid & 31, warp = tid >> 5;
+  const int cta = blockIdx.x, lane = threadIdx.x & 31, c = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int4 m0 = *reinterpret_cast<const int4*>(a.meta + (int64_t)cta * kMetaInts);
   const int2 m1 = *reinterpret_cast<const int2*>(a.meta + (int64_t)cta * kMetaInts + 4);
   if (m0.x == 0) return;
   const Shape s = shape_of<NC>(a);
   const int hh = m0.z, qb = m0.w, q0 = m1.x, nq = m1.y, hb = hh % s.nhb;
-  if (qb * s.QB + c0 / s.HB >= nq) return;  // no query in these columns
-  const int n = m0.y + 1 - cta;             // piece i is CTA cta + i's
+  const int qi = c / s.HB, head = c - qi * s.HB, i = qb * s.QB + qi;
+  if (qi >= s.QB || i >= nq || head >= s.G - hb * s.HB) return;  // no query in this column
+  const int n = m0.y + 1 - cta;                                  // piece k is CTA cta + k's
   const float* part = a.part + (int64_t)cta * 2 * kPart;
-  const auto piece = [&](int i) { return part + (i == 0 ? kPart : (int64_t)i * 2 * kPart); };
-  const auto stats = [&](int i, int j) { return *reinterpret_cast<const float2*>(piece(i) + NC * HD + 2 * (c0 + j)); };
-  for (int j = warp; j < 8; j += kWarps) {
-    float M = -INFINITY, l = 0.0f;
-    for (int i = lane; i < n; i += 32) {
-      const float2 v = stats(i, j);
-      if (v.y != 0.0f) {  // a piece that saw no key has no maximum
-        const float top = fmaxf(M, v.x);
-        l = l * exp2f(M - top) + v.y * exp2f(v.x - top);
-        M = top;
-      }
-    }
-    float top = M;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    l = l != 0.0f ? l * exp2f(M - top) : 0.0f;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane == 0) {
-      s_m[j] = top;
-      s_l[j] = l;
-    }
+  const auto piece = [&](int k) { return part + (k == 0 ? kPart : (int64_t)k * 2 * kPart); };
+  const auto stats = [&](int k) {  // maximum and sum; a piece that saw no key has sum 0 and no maximum
+    return k < n ? *reinterpret_cast<const float2*>(piece(k) + NC * HD + 2 * c) : make_float2(0.0f, 0.0f);
+  };
+  float M = -INFINITY;
+  for (int k = lane; k < n; k += 32) {
+    const float2 v = stats(k);
+    if (v.y != 0.0f) M = fmaxf(M, v.x);
   }
-  float acc[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
-  for (int i0 = 0; i0 < n; i0 += kChunk) {
-    const int in = n - i0 < kChunk ? n - i0 : kChunk;
-    __syncthreads();
-    for (int k = tid; k < in * 8; k += kThreads) {
-      const float2 v = stats(i0 + k / 8, k % 8);
-      s_w[k / 8][k % 8] = v.y != 0.0f ? exp2f(v.x - s_m[k % 8]) : 0.0f;
-    }
-    __syncthreads();
-#pragma unroll 4
-    for (int i = split; i < in; i += kMergeSplit) {
-      const float* p = piece(i0 + i) + c0 * HD + d;
-      float o[8];
+  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float l = 0.0f, acc[kPer];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = p[j * HD];
+  for (int d = 0; d < kPer; ++d) acc[d] = 0.0f;
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    const float2 v = stats(k0 + lane);
+    const float w = v.y != 0.0f ? exp2f(v.x - M) : 0.0f;
+    l += v.y != 0.0f ? v.y * w : 0.0f;
+    const int in = n - k0 < 32 ? n - k0 : 32;
+#pragma unroll 8
+    for (int k = 0; k < in; ++k) {
+      const Vec o = *reinterpret_cast<const Vec*>(piece(k0 + k) + c * HD + lane * kPer);
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      const float* x = reinterpret_cast<const float*>(&o);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float w = s_w[i][j];
-        acc[j] = w != 0.0f ? fmaf(o[j], w, acc[j]) : acc[j];  // columns without a row hold any bits
-      }
+      for (int d = 0; d < kPer; ++d) acc[d] = fmaf(x[d], wk, acc[d]);
     }
   }
-  if (split > 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s_acc[split - 1][j][d] = acc[j];
-  }
-  __syncthreads();
-  if (split > 0) return;
+  for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const int64_t to = (int64_t)(q0 + i) * a.Hq + hh / s.nhb * s.G + hb * s.HB + head;
+  T* out = reinterpret_cast<T*>(a.out) + to * HD + lane * kPer;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int c = c0 + j, qi = c / s.HB, hd = c - qi * s.HB, i = qb * s.QB + qi;
-    if (qi >= s.QB || i >= nq || hd >= s.G - hb * s.HB) continue;
-    const int64_t to = (int64_t)(q0 + i) * a.Hq + hh / s.nhb * s.G + hb * s.HB + hd;
-    const float l = s_l[j];
-    float o = acc[j];
-#pragma unroll
-    for (int k = 0; k < kMergeSplit - 1; ++k) o += s_acc[k][j][d];
-    reinterpret_cast<T*>(a.out)[to * HD + d] = from_float<T>(l != 0.0f ? __fdiv_rn(o, l) : 0.0f);
-    if (a.lse && d == 0) a.lse[to] = l != 0.0f ? (s_m[j] + log2f(l) - lift) * kLn2 : -INFINITY;
-  }
+  for (int d = 0; d < kPer; ++d) out[d] = from_float<T>(l != 0.0f ? __fdiv_rn(acc[d], l) : 0.0f);
+  if (a.lse && lane == 0) a.lse[to] = l != 0.0f ? (M + log2f(l) - lift) * kLn2 : -INFINITY;
 }
 
 // kv8_wide.cu: the kernel for many rows per key head.

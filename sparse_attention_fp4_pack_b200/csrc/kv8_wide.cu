@@ -6,7 +6,7 @@
 // once: both products are then tcgen05.mma kind::f16 at one column per score, where the digit
 // form of kv8_attn.cu needs two or three.  f16 holds every code exactly.  A query row enters as
 // f16 after a power of two has brought its largest element into [2^14, 2^15): exact for bf16 and
-// fp16 down to 2^-28 of that element.  Probabilities are rounded to f16 under a shift of 2^12.
+// fp16 down to 2^-28 of that element.  Probabilities are rounded to f16 under a shift of 2^4.
 //   S[128 rows x 128 keys] = Q . K_tile^T,   O[128 rows x hd] += P . V_tile  (P from tensor memory)
 // A page's K scale times the row's scale multiplies the scores of its keys, and log2(v_scale)
 // is added: one fused multiply-add per score.  exp2 of that is the weight of the key's V codes,
@@ -20,7 +20,7 @@
 //
 // Roles: warps 0-3 and 4-7 softmax of slot 0 and 1; warp 13 brings tiles from their pages by TMA
 // in the order K0 K1 V0 K2 V1 K3 ...; warps 8-11 turn them into f16 in a ring of shared memory
-// tiles; one thread of warp 12 issues the products.  Every wait is bounded: on expiry the CTA
+// tiles; warp 12 issues the products.  Every wait is bounded: on expiry the CTA
 // flags CSA2_DEV_TIMEOUT, drains its copies and products and returns.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -36,7 +36,11 @@
 
 namespace csa2 {
 
-constexpr float kWideLift = 12.0f;  // probabilities are 2^(t - max + 12), at most 2^14
+// Probabilities are 2^(t - m + 4) with m raised only when a score exceeds it by more than 10, so
+// they stay below f16's 2^15 and what f16 drops is below 2^-28 of the largest.  The accumulated
+// output is rescaled on a raise; with a slack of 2 one tile in five did (a softmax warp's 561 of
+// 3350 cycles per tile).
+constexpr float kWideLift = 4.0f, kWideSlack = 10.0f;
 
 template <int HD, bool CAP_>
 struct KvWide {
@@ -59,7 +63,7 @@ template <class C>
 struct WideShared {
   uint64_t rfull[C::kStages], rempty[C::kStages];  // tiles as E4M3
   uint64_t full[C::kRing], empty[C::kRing];        // tiles as f16
-  uint64_t qfull[2], sfull[2], pfull[2], ofull[2], drain;
+  uint64_t qfull[2], sfull[2], pfull[2][2], ofull[2], drain;  // pfull: by half of the keys
   uint32_t tmem;
   int abort;
   Share share;
@@ -73,6 +77,31 @@ template <int N>
 __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Two fp32 operations per instruction on neighbouring registers, and a three-way maximum.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 // All 128 score columns of this thread's TMEM lane: four loads in flight, one wait.  The empty
 // statements keep every use of the values behind the wait.
@@ -178,11 +207,41 @@ __device__ void load_tiles(const KvAttnArgs& a, const Shape& s, WideShared<C>& s
 }
 
 // ---- E4M3 tiles to f16 tiles (128 threads) -------------------------------------------------
+// A thread turns 8 codes into one 16-byte chunk at a time; its rows differ by multiples of 8, so
+// the swizzle is the same for all of them.
+template <class C, bool kAll>
+__device__ __forceinline__ void convert_tile(uint32_t from, uint32_t to, int row0, int lo, int hi, uint32_t pages,
+                                             int page_log2) {
+  constexpr int kStep = 1024 / C::kHD;  // rows per 128 threads
+  constexpr int kBatch = 8;  // loads in flight
+#pragma unroll
+  for (int b = 0; b < kKeys / kStep; b += kBatch) {
+    uint32_t x[kBatch][2];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[k][0]), "=r"(x[k][1]) : "r"(from + (b + k) * 1024) : "memory");
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if constexpr (!kAll) {
+        // what no key of the block fills may be any bits: zeros, which zero probabilities keep
+        const int row = row0 + (b + k) * kStep;
+        if (row < lo || row >= hi || !((pages >> (row >> page_log2)) & 1u)) x[k][0] = x[k][1] = 0u;
+      }
+      tc::st_shared_v4(to + (b + k) * (kStep * 128),
+                       make_uint4(f16x2_of_e4m3x2(x[k][0] & 0xFFFFu), f16x2_of_e4m3x2(x[k][0] >> 16),
+                                  f16x2_of_e4m3x2(x[k][1] & 0xFFFFu), f16x2_of_e4m3x2(x[k][1] >> 16)));
+    }
+  }
+}
+
 template <class C>
 __device__ void convert_tiles(const KvAttnArgs& a, WideShared<C>& sh, uint32_t smem) {
-  constexpr int kChunks = C::kHD / 16;  // 16-byte chunks per row of codes
-  const int tid = threadIdx.x & 127;
-  const uint32_t chunk = tid % kChunks, odd = chunk >= 4 ? 1u : 0u;
+  constexpr int kChunks = C::kHD / 8;  // 8-code chunks per row
+  const int tid = threadIdx.x & 127, row0 = tid / kChunks;
+  const uint32_t chunk = tid % kChunks;
+  const uint32_t from = smem + C::kOffRaw + tid * 8;
+  const uint32_t to = smem + C::kOffRing + (chunk / 8) * C::kHalf + row0 * 128 + (((chunk ^ row0) & 7u) << 4);
+  const uint32_t every = (1u << (kKeys >> a.page_log2)) - 1u;
   const int64_t items = 2 * sh.share.left;
   for (uint32_t n = 0; n < items; ++n) {
     const uint32_t st = n % C::kStages, slot = n % C::kRing;
@@ -191,35 +250,20 @@ __device__ void convert_tiles(const KvAttnArgs& a, WideShared<C>& sh, uint32_t s
     if (!__all_sync(0xffffffffu, ok)) return;
     const int lo = sh.rows[st][0], hi = sh.rows[st][1];
     const uint32_t pages = sh.pages[st];
-    const uint32_t from = smem + C::kOffRaw + st * C::kRaw + tid * 16;
-    const uint32_t to = smem + C::kOffRing + slot * C::kTile + (chunk / 4) * C::kHalf;
-#pragma unroll 4
-    for (int k = 0; k < C::kHD / 16; ++k) {
-      const int row = k * (128 / kChunks) + tid / kChunks;
-      uint4 v = tc::ld_shared_v4(from + k * 2048);
-      // what no key of the block fills may be any bits: zeros, which zero probabilities keep
-      if (row < lo || row >= hi || !((pages >> (row >> a.page_log2)) & 1u)) v = make_uint4(0u, 0u, 0u, 0u);
-      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-      uint32_t y[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y[2 * i] = f16x2_of_e4m3x2(x[i] & 0xFFFFu);
-        y[2 * i + 1] = f16x2_of_e4m3x2(x[i] >> 16);
-      }
-      // 16-byte chunks 2 chunk and 2 chunk + 1 of the row; lanes of the second 64 channels go
-      // the other way round, so the eight lanes of a row use eight different banks
-      const uint32_t at = to + row * 128;
-      const uint32_t p0 = (2 * (chunk & 3) + odd) ^ (row & 7), p1 = (2 * (chunk & 3) + 1 - odd) ^ (row & 7);
-      tc::st_shared_v4(at + (p0 << 4), odd ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]));
-      tc::st_shared_v4(at + (p1 << 4), odd ? make_uint4(y[0], y[1], y[2], y[3]) : make_uint4(y[4], y[5], y[6], y[7]));
-    }
+    if (lo <= 0 && hi >= kKeys && pages == every)
+      convert_tile<C, true>(from + st * C::kRaw, to + slot * C::kTile, row0, lo, hi, pages, a.page_log2);
+    else
+      convert_tile<C, false>(from + st * C::kRaw, to + slot * C::kTile, row0, lo, hi, pages, a.page_log2);
     tc::fence_async_smem();
-    tc::mbar_arrive(tc::smem_u32(&sh.full[slot]));
-    tc::mbar_arrive(tc::smem_u32(&sh.rempty[st]));
+    __syncwarp();
+    if ((tid & 31) == 0) {  // one arrival per warp
+      tc::mbar_arrive(tc::smem_u32(&sh.full[slot]));
+      tc::mbar_arrive(tc::smem_u32(&sh.rempty[st]));
+    }
   }
 }
 
-// ---- products (one thread) -----------------------------------------------------------------
+// ---- products (one warp) --------------------------------------------------------------------
 template <class C>
 __device__ void multiply_wide(WideShared<C>& sh, uint32_t smem, uint32_t tmem) {
   constexpr uint32_t kIdS = tc::idesc_f16(128, kKeys, false, false);
@@ -229,39 +273,43 @@ __device__ void multiply_wide(WideShared<C>& sh, uint32_t smem, uint32_t tmem) {
   const uint64_t dv0 = tc::smem_desc_sw128(smem + C::kOffRing, C::kHalf, 1024);
   uint32_t base = 0, piece = 0;  // ring items of the pieces before; pieces
   uint32_t np[2] = {0, 0};       // probabilities consumed per slot
+  const bool on = (threadIdx.x & 31) == 0;
   bool ok = true;
   int take = 0;
   auto ring = [&](int i, bool v) {  // ring item of tile i of this piece
     return base + (v ? (i + 1 < take ? 2 * i + 2 : 2 * i + 1) : (i > 0 ? 2 * i - 1 : 0));
   };
   auto tile_there = [&](uint32_t item) {
-    return kv_wait(&sh.abort, sh.full[item % C::kRing], (item / C::kRing) & 1u);
+    return kv_wait_all(sh, sh.full[item % C::kRing], (item / C::kRing) & 1u);
   };
-  auto release = [&](uint32_t item) { tc::commit(tc::smem_u32(&sh.empty[item % C::kRing])); };
+  auto release = [&](uint32_t item) { commit_if(on, tc::smem_u32(&sh.empty[item % C::kRing])); };
   auto scores = [&](uint32_t item, int q, int g) {
     const uint64_t dk = tc::desc_add(dk0, (item % C::kRing) * C::kTile), dq = tc::desc_add(dq0, q * C::kTile);
 #pragma unroll
     for (int k = 0; k < C::kHD / 16; ++k) {
       const uint32_t o = (k / 4) * C::kHalf + (k % 4) * 32;
-      tc::mma_f16(tmem + g * 128, tc::desc_add(dq, o), tc::desc_add(dk, o), kIdS, k > 0);
+      mma_ss(on, tmem + g * 128, tc::desc_add(dq, o), tc::desc_add(dk, o), kIdS, k > 0);
     }
-    tc::commit(tc::smem_u32(&sh.sfull[g]));
+    commit_if(on, tc::smem_u32(&sh.sfull[g]));
   };
   auto outputs = [&](uint32_t item, int g, bool fresh) {
-    ok = kv_wait(&sh.abort, sh.pfull[g], np[g] & 1u);
-    if (!ok) return;
-    ++np[g];
-    tc::fence_after_sync();
     const uint64_t dv = tc::desc_add(dv0, (item % C::kRing) * C::kTile);
 #pragma unroll
-    for (int k = 0; k < kKeys / 16; ++k)
-      tc::mma_f16_ts(tmem + C::kColO + g * C::kHD, tmem + g * 128 + k * 8, tc::desc_add(dv, k * 2048), kIdO, !fresh || k > 0);
+    for (int q = 0; q < 2; ++q) {
+      ok = kv_wait_all(sh, sh.pfull[g][q], np[g] & 1u);
+      if (!ok) return;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int k = 4 * q; k < 4 * q + 4; ++k)
+        mma_ts(on, tmem + C::kColO + g * C::kHD, tmem + g * 128 + k * 8, tc::desc_add(dv, k * 2048), kIdO, !fresh || k > 0);
+    }
+    ++np[g];
   };
-  for (int64_t left = sh.share.left; ok && left > 0; left -= take, ++piece) {
-    ok = kv_wait(&sh.abort, sh.qfull[0], piece & 1u) && kv_wait(&sh.abort, sh.qfull[1], piece & 1u);
+  for (int left = uniform((int)sh.share.left); ok && left > 0; left -= take, ++piece) {
+    ok = kv_wait_all(sh, sh.qfull[0], piece & 1u) && kv_wait_all(sh, sh.qfull[1], piece & 1u);
     if (!ok) break;
-    take = sh.take;
-    const bool one_slot = sh.one_slot != 0;
+    take = uniform(sh.take);
+    const bool one_slot = uniform(sh.one_slot) != 0;
     ok = tile_there(ring(0, false));
     if (!ok) break;
     tc::fence_after_sync();
@@ -275,20 +323,18 @@ __device__ void multiply_wide(WideShared<C>& sh, uint32_t smem, uint32_t tmem) {
         release(ring(1, false));
       }
       for (int i = 0; ok && i < take; ++i) {
-        ok = tile_there(ring(i, true));
+        ok = tile_there(ring(i, true)) && (i + 2 >= take || tile_there(ring(i + 2, false)));
         if (ok) outputs(ring(i, true), i & 1, i < 2);
         if (!ok) break;
         release(ring(i, true));
         if (i + 2 < take) {
-          ok = tile_there(ring(i + 2, false));
-          if (!ok) break;
           scores(ring(i + 2, false), 0, i & 1);
           release(ring(i + 2, false));
         }
       }
       if (ok) {
-        tc::commit(tc::smem_u32(&sh.ofull[0]));
-        tc::commit(tc::smem_u32(&sh.ofull[1]));
+        commit_if(on, tc::smem_u32(&sh.ofull[0]));
+        commit_if(on, tc::smem_u32(&sh.ofull[1]));
       }
     } else {
       scores(ring(0, false), 0, 0);
@@ -296,21 +342,16 @@ __device__ void multiply_wide(WideShared<C>& sh, uint32_t smem, uint32_t tmem) {
       release(ring(0, false));
       for (int i = 0; ok && i < take; ++i) {
         const bool last = i + 1 == take;
-        ok = tile_there(ring(i, true));
+        ok = tile_there(ring(i, true)) && (last || tile_there(ring(i + 1, false)));
         if (ok) outputs(ring(i, true), 0, i == 0);
         if (!ok) break;
-        if (last) {
-          tc::commit(tc::smem_u32(&sh.ofull[0]));
-        } else {
-          ok = tile_there(ring(i + 1, false));
-          if (!ok) break;
-          scores(ring(i + 1, false), 0, 0);
-        }
+        if (last) commit_if(on, tc::smem_u32(&sh.ofull[0]));
+        else scores(ring(i + 1, false), 0, 0);
         outputs(ring(i, true), 1, i == 0);
         if (!ok) break;
         release(ring(i, true));
         if (last) {
-          tc::commit(tc::smem_u32(&sh.ofull[1]));
+          commit_if(on, tc::smem_u32(&sh.ofull[1]));
         } else {
           scores(ring(i + 1, false), 1, 1);
           release(ring(i + 1, false));
@@ -320,7 +361,7 @@ __device__ void multiply_wide(WideShared<C>& sh, uint32_t smem, uint32_t tmem) {
     base += 2 * take;
   }
   if (!ok) {  // given up: no product may run after the tensor memory is freed
-    tc::commit(tc::smem_u32(&sh.drain));
+    commit_if(on, tc::smem_u32(&sh.drain));
     tc::mbar_wait(tc::smem_u32(&sh.drain), 0, kKvPolls);
   }
 }
@@ -393,7 +434,8 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
         sh.one_slot = shared_rows;
       }
       tc::fence_async_smem();
-      tc::mbar_arrive(tc::smem_u32(&sh.qfull[g]));
+      __syncwarp();
+      if ((tid & 31) == 0) tc::mbar_arrive(tc::smem_u32(&sh.qfull[g]));
     }
     // keys that every row of the block sees: the first query ends soonest, the last starts latest
     const int last_q = (w.qb + 1) * s.QB < w.x.n ? (w.qb + 1) * s.QB - 1 : w.x.n - 1;
@@ -425,9 +467,9 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
             t.f[k] = fmaf(cap2, 1.0f - __fdividef(2.0f, 1.0f + e2), off);
           }
         } else {
-          const float k2 = x.x * qs, off = x.y + shift;
+          const uint64_t k2 = pack2(x.x * qs, x.x * qs), off = pack2(x.y + shift, x.y + shift);
 #pragma unroll
-          for (int k = p * 16; k < p * 16 + 16; ++k) t.f[k] = fmaf(t.f[k], k2, off);
+          for (int k = p * 16; k < p * 16 + 16; k += 2) unpack2(fma2(pack2(t.f[k], t.f[k + 1]), k2, off), t.f[k], t.f[k + 1]);
         }
       }
       if (key0 + kKeys > all_hi || key0 < all_lo) {
@@ -438,9 +480,13 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
       }
       float mx[4] = {t.f[0], t.f[1], t.f[2], t.f[3]};
 #pragma unroll
-      for (int k = 4; k < 128; ++k) mx[k & 3] = fmaxf(mx[k & 3], t.f[k]);
+      for (int k = 4; k + 7 < 128; k += 8)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) mx[x] = max3(mx[x], t.f[k + 2 * x], t.f[k + 2 * x + 1]);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], t.f[124 + x]);
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) - kWideLift;
-      const bool raise = fresh ? top > -INFINITY : top > kSlack;
+      const bool raise = fresh ? top > -INFINITY : top > kWideSlack;
       if (__any_sync(0xffffffffu, raise)) {
         const float up = raise ? top : 0.0f, f = fresh ? 1.0f : exp2_approx(-up);
         m += up;
@@ -464,22 +510,24 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
         uint32_t pk[32];
 #pragma unroll
         for (int p = 4 * q; p < 4 * q + 4; ++p) {
-          float sum[2] = {0.0f, 0.0f};
+          uint64_t sum = pack2(0.0f, 0.0f);
 #pragma unroll
           for (int k = p * 16; k < p * 16 + 16; k += 2) {
             const float p0 = exp2_approx(t.f[k]), p1 = exp2_approx(t.f[k + 1]);
-            sum[0] += p0;
-            sum[1] += p1;
+            sum = add2(sum, pack2(p0, p1));
             const __half2 v = __floats2half2_rn(p0, p1);
             pk[k / 2 - q * 32] = *reinterpret_cast<const uint32_t*>(&v);
           }
-          l = fmaf(sum[0] + sum[1], sc[(p * 16) >> a.page_log2].z, l);
+          float even, odd;
+          unpack2(sum, even, odd);
+          l = fmaf(even + odd, sc[(p * 16) >> a.page_log2].z, l);
         }
         tc::tmem_st32_nowait(s_at + q * 32, pk);
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if ((tid & 31) == 0) tc::mbar_arrive(tc::smem_u32(&sh.pfull[g][q]));  // the products of these 64 keys may start
       }
-      tc::tmem_wait_st();
-      tc::fence_before_sync();
-      tc::mbar_arrive(tc::smem_u32(&sh.pfull[g]));
     }
     tile0 += w.take;
     if (!bad) bad = !__all_sync(0xffffffffu, kv_wait(&sh.abort, sh.ofull[g], piece & 1u));
@@ -553,20 +601,21 @@ __global__ void __launch_bounds__(C::kThreads, 1) kv8_wide_kernel(const __grid_c
   extern __shared__ uint8_t raw[];
   __shared__ WideShared<C> sh;
   uint8_t* smem = tc::align_smem_1024(raw);
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5);
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       tc::mbar_init(tc::smem_u32(&sh.rfull[i]), 1);
-      tc::mbar_init(tc::smem_u32(&sh.rempty[i]), 128);
+      tc::mbar_init(tc::smem_u32(&sh.rempty[i]), 4);
     }
     for (int i = 0; i < C::kRing; ++i) {
-      tc::mbar_init(tc::smem_u32(&sh.full[i]), 128);
+      tc::mbar_init(tc::smem_u32(&sh.full[i]), 4);
       tc::mbar_init(tc::smem_u32(&sh.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(tc::smem_u32(&sh.qfull[i]), 128);
+      tc::mbar_init(tc::smem_u32(&sh.qfull[i]), 4);
       tc::mbar_init(tc::smem_u32(&sh.sfull[i]), 1);
-      tc::mbar_init(tc::smem_u32(&sh.pfull[i]), 128);
+      tc::mbar_init(tc::smem_u32(&sh.pfull[i][0]), 4);
+      tc::mbar_init(tc::smem_u32(&sh.pfull[i][1]), 4);
       tc::mbar_init(tc::smem_u32(&sh.ofull[i]), 1);
     }
     tc::mbar_init(tc::smem_u32(&sh.drain), 1);
@@ -583,7 +632,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) kv8_wide_kernel(const __grid_c
   __syncthreads();
   tc::fence_after_sync();
   chain_launch_dependents();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = uniform(sh.tmem);
   if (warp < 8) {
     reg_inc<C::kRegsSoft>();
     soften_wide<C, T>(a, s, sh, smem, tmem);
@@ -592,7 +641,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) kv8_wide_kernel(const __grid_c
     convert_tiles<C>(a, sh, tc::smem_u32(smem));
   } else {
     reg_dec<C::kRegsMma>();
-    if (tid == 12 * 32) multiply_wide<C>(sh, tc::smem_u32(smem), tmem);
+    if (warp == 12) multiply_wide<C>(sh, tc::smem_u32(smem), tmem);
     else if (warp == 13) load_tiles<C>(a, s, sh, tc::smem_u32(smem), &kmap, &vmap);
   }
   __syncwarp();
@@ -622,7 +671,7 @@ static cudaError_t launch_wide_t(KvAttnArgs a, const CUtensorMap& km, const CUte
   if (e != cudaSuccess) return e;
   e = launch_chained(kv8_wide_kernel<C, T>, dim3(num_sms), dim3(C::kThreads), C::kSmem, stream, 0, km, vm, a);
   if (e != cudaSuccess) return e;
-  e = launch_chained(kv8_merge_kernel<C::NC, C::kHD, T>, dim3(num_sms, C::NC / 8), dim3(C::kHD * kMergeSplit), 0,
+  e = launch_chained(kv8_merge_kernel<C::NC, C::kHD, T>, dim3(num_sms, C::NC / 8), dim3(kMergeThreads), 0,
                      stream, 0, a, kWideLift);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
