@@ -9,6 +9,7 @@ is no other code path.  Workspaces are plain uint8 device tensors from torch's
 allocator (``workspace``).
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -650,6 +651,13 @@ def csa2_kv8_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, dev_stat
            "csa2_kv8_append")
 
 
+@functools.lru_cache(maxsize=256)
+def _kv8_ws(dev, Hq, Hk, hd, max_q, kind):
+    """Workspace bytes on cuda:`dev` (by its number of SMs); at least 1, refusals come from the call."""
+    with torch.cuda.device(dev):
+        return max(lib().csa2_kv8_attn_workspace_size(Hq, Hk, hd, max_q, kind), 1)
+
+
 def csa2_kv8_attn_workspace_size(Hq, Hk, hd, max_q, dtype=torch.bfloat16):
     return lib().csa2_kv8_attn_workspace_size(Hq, Hk, hd, max_q, _KV_DTYPES[dtype])
 
@@ -673,16 +681,12 @@ def csa2_kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, q_start, s
     L = lib()
     if ws is None:
         # taken on the stream that uses it, so the allocator keeps it until the kernels are done
-        if torch.cuda.current_device() == dev:
-            need = L.csa2_kv8_attn_workspace_size(Hq, Hk, hd, max_q, kind)
-        else:  # it goes by the device's number of SMs
-            with torch.cuda.device(dev):
-                need = L.csa2_kv8_attn_workspace_size(Hq, Hk, hd, max_q, kind)
+        need = _kv8_ws(dev, Hq, Hk, hd, max_q, kind)
         if stream is None:
-            ws = workspace(need, q.device)
+            ws = q.new_empty(need, dtype=_U8)
         else:
             with torch.cuda.stream(stream):
-                ws = workspace(need, q.device)
+                ws = q.new_empty(need, dtype=_U8)
     elif ws.dtype is not _U8 or ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous uint8 tensor on cuda:{dev}")
     _check(_call_on(

@@ -19,9 +19,12 @@
 // the tiles each block sees.  CTA c takes the c-th of equal shares of it; an item cut by a
 // share's border leaves partial sums in the workspace and kv8_merge_kernel joins them.
 //
-// Roles: warps 0-3 (0-7 with 64 columns) softmax, then one producer warp (TMA, page ids,
-// scales) and one warp that issues the products.  Every wait is bounded: on expiry the CTA
-// flags CSA2_DEV_TIMEOUT, drains its copies and products, frees its tensor memory and returns.
+// Roles: warps 0-3 softmax, then one producer warp (TMA, page ids, scales, queries)
+// and one warp that issues the products.  The producer works ahead: a piece's tiles, query rows
+// and description are on their way while the one before is computed, and the softmax warps turn
+// the rows into digits before they write the previous piece's output.  Every wait is bounded: on
+// expiry the CTA flags CSA2_DEV_TIMEOUT, drains its copies and products, frees its tensor memory
+// and returns.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -48,19 +51,18 @@ struct KvCfg {
   static constexpr bool CAP = CAP_;
   static constexpr int NS = round16(NC * DQ);   // columns of S
   static constexpr int NP = round16(NC * 3);    // columns of O
-  static constexpr int kGroups = NC == 64 ? 2 : 1;  // softmax warpgroups
-  static constexpr int CW = NC / kGroups;           // columns per softmax thread
-  static constexpr int kSoft = 128 * kGroups;
-  static constexpr int kThreads = kSoft + 64;
+  static constexpr int kSoft = 128, kThreads = kSoft + 64;
   static constexpr uint32_t kTile = kKeys * HD;  // bytes of a K or V tile
   static constexpr uint32_t kQBytes = (NS * HD + 1023) / 1024 * 1024;
   static constexpr uint32_t kPBytes = NP * kKeys;
+  static constexpr uint32_t kRawBytes = NC * HD * 2;  // query rows as they come
   static constexpr int kCtas = NC <= 16 ? 2 : 1;  // per SM
   static constexpr uint32_t kBudget = (kCtas == 2 ? 112u : 224u) * 1024u - 4096u;
-  static constexpr int kFit = (int)((kBudget - kQBytes - kPBytes) / (2 * kTile));
+  static constexpr int kFit = (int)((kBudget - 2 * kQBytes - kPBytes - 2 * kRawBytes) / (2 * kTile));
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
-  static constexpr uint32_t kOffK = 0, kOffV = kStages * kTile, kOffQ = 2 * kStages * kTile, kOffP = kOffQ + kQBytes;
-  static constexpr uint32_t kSmem = kOffP + kPBytes + 1024;  // + alignment slack
+  static constexpr uint32_t kOffK = 0, kOffV = kStages * kTile, kOffQ = 2 * kStages * kTile, kOffP = kOffQ + 2 * kQBytes;
+  static constexpr uint32_t kOffRaw = kOffP + kPBytes;
+  static constexpr uint32_t kSmem = kOffRaw + 2 * kRawBytes + 1024;  // + alignment slack
   static constexpr uint32_t kColS = 0, kColO = 2 * NS;
   static constexpr uint32_t kCols = pow2_cols(2 * NS + NP);
   static constexpr uint32_t kSwz = tc::swizzle_code(HD);
@@ -124,18 +126,157 @@ __device__ __forceinline__ uint32_t rest16(uint32_t p, uint32_t d) {  // (p - d)
 template <class C>
 struct KvShared {
   uint64_t kfull[C::kStages], kempty[C::kStages], vfull[C::kStages], vempty[C::kStages];
-  uint64_t sfull[2], sfree[2], qfull, pfull, pvdone, drain;
+  uint64_t sfull[2], sfree[2], rows[2], qfull[2], qfree[2], pfull, pvdone, drain;
   uint32_t tmem;
   int abort;
   Share share;
-  int64_t sums[C::kThreads];
+  int64_t sums[C::kThreads / 32];
   float ks[C::kStages][kMaxTilePages], vs[C::kStages][kMaxTilePages];
-  float qscale[C::NC];
-  int col_lo[C::NC], col_hi[C::NC];
-  int64_t col_row[C::NC];  // row of out / lse (token * Hq + head), -1 for padding columns
-  float red[C::kGroups][4][C::CW];
+  struct Piece {           // two are kept, the next one's description comes early
+    int take, tile;        // its tiles, and the first one's place in the request
+    int lo, hi;            // keys that any of its columns sees,
+    int all_lo, all_hi;    // that every column sees
+    int first, whole;      // it starts its item, it is all of it
+    int q0, n, i0, pos0;   // first row and number of queries of the request, the block's first query, its position
+    int cap;               // keys of the request
+    int head0, heads;      // first query head of the block, number of them
+  } piece[2];
+  struct Column {  // of the queries of a piece
+    float qscale;
+    int lo, hi;    // keys it sees
+    int row;       // of out / lse (token * Hq + head), -1 for padding columns
+  } col[2][C::NC];
+  float red[4][C::NC];
   float linv[C::NC];
 };
+
+// ---- queries -----------------------------------------------------------------------------
+// One warp: a piece's description, and its query rows on their way.
+template <class C>
+__device__ __forceinline__ void fetch_queries(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uint32_t smem,
+                                              const Walk& w, int buf) {
+  constexpr int kChunks = C::kHD / 8;  // of 16 bytes per row
+  const int lane = threadIdx.x & 31;
+  const int h = w.hh / s.nhb, hb = w.hh - h * s.nhb;
+  const int nh = s.G - hb * s.HB < s.HB ? s.G - hb * s.HB : s.HB, head0 = h * s.G + hb * s.HB, i0 = w.qb * s.QB;
+#pragma unroll 1
+  for (int x = lane; x < C::NC * kChunks; x += 32) {
+    const int c = x / kChunks, qi = c / s.HB, hd = c - qi * s.HB;
+    if (qi < s.QB && i0 + qi < w.x.n && hd < nh)
+      tc::cp_async16(smem + C::kOffRaw + buf * C::kRawBytes + x * 16,
+                     a.q + (int64_t)(w.x.q0 + i0 + qi) * a.q_stride + (int64_t)(head0 + hd) * (C::kHD * 2) + (x % kChunks) * 16);
+  }
+  const uint32_t bar = tc::smem_u32(&sh.rows[buf]);
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+  if (lane == 0) {
+    // the block's first query ends soonest, its last starts latest
+    const int last_q = i0 + s.QB < w.x.n ? i0 + s.QB - 1 : w.x.n - 1;
+    const int64_t all_hi = (int64_t)w.x.pos0 + i0 + 1;
+    const int64_t all_lo = a.window > 0 ? (int64_t)w.x.pos0 + last_q + 1 - a.window : 0;
+    auto& p = sh.piece[buf];
+    p.take = w.take;
+    p.tile = w.g.tile + w.off;
+    p.lo = w.g.lo;
+    p.hi = w.g.hi;
+    p.all_hi = all_hi < 0 ? 0 : (all_hi < w.x.cap ? (int)all_hi : w.x.cap);
+    p.all_lo = all_lo < 0 ? 0 : (all_lo < 0x7FFFFFFF ? (int)all_lo : 0x7FFFFFFF);
+    p.first = w.first;
+    p.whole = w.first && w.last;
+    p.q0 = w.x.q0;
+    p.n = w.x.n;
+    p.i0 = i0;
+    p.pos0 = w.x.pos0 + i0;
+    p.cap = w.x.cap;
+    p.head0 = head0;
+    p.heads = nh;
+    tc::mbar_arrive(bar);
+    if (w.first && !w.last) note_item(a, sh.share, w);
+  }
+}
+
+// The softmax warps: the piece's query rows as E4M3 digits (row d * NC + column of the Q
+// operand), and what each column needs later.  A warp's columns do not wait for one another.
+template <class C, typename T>
+__device__ __forceinline__ bool prepare_queries(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uint32_t smem,
+                                                uint32_t piece) {
+  constexpr int kPer = C::kHD / 32, kCols = C::NC / 4;  // elements per lane, columns per warp
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, buf = (int)(piece & 1u);
+  if (!kv_wait(&sh.abort, sh.rows[buf], (piece >> 1) & 1u)) return false;
+  const auto& p = sh.piece[buf];
+  const int i0 = p.i0, n = p.n, heads = p.heads;
+  float x[kCols][kPer], amax[kCols];
+  int qi[kCols], hd[kCols];
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) {
+    const int c = k * 4 + warp;
+    qi[k] = c / s.HB;
+    hd[k] = c - qi[k] * s.HB;
+    uint32_t raw[kPer / 2];
+    const uint32_t at = smem + C::kOffRaw + buf * C::kRawBytes + c * (C::kHD * 2) + lane * (kPer * 2);
+    if constexpr (kPer == 4)
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(raw[0]), "=r"(raw[1]) : "r"(at) : "memory");
+    else raw[0] = tc::ld_shared_u32(at);
+    if (!(qi[k] < s.QB && i0 + qi[k] < n && hd[k] < heads)) {
+      qi[k] = -1;  // a padding column: its row was not brought
+#pragma unroll
+      for (int e = 0; e < kPer / 2; ++e) raw[e] = 0;
+    }
+    float top = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kPer / 2; ++e) {
+      if constexpr (std::is_same<T, __half>::value) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&raw[e]));
+        x[k][2 * e] = f.x;
+        x[k][2 * e + 1] = f.y;
+      } else {
+        x[k][2 * e] = bf16_lo(raw[e]);
+        x[k][2 * e + 1] = bf16_hi(raw[e]);
+      }
+      top = fmaxf(top, fmaxf(fabsf(x[k][2 * e]), fabsf(x[k][2 * e + 1])));
+    }
+    amax[k] = top;
+  }
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) amax[k] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax[k])));
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) {
+    const int c = k * 4 + warp;
+    int e = (int)(__float_as_uint(amax[k]) >> 23) - 127;  // amax in [2^e, 2^(e+1))
+    e = e < -100 ? -100 : e;
+    const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[k][i] *= up;
+#pragma unroll
+    for (int d = 0; d < C::DQ; ++d) {
+      uint32_t word = 0;
+#pragma unroll
+      for (int i = 0; i < kPer / 2; ++i) {
+        const uint32_t b = e4m3x2_sat(x[k][2 * i], x[k][2 * i + 1]);
+        word |= b << (16 * i);
+        const uint32_t back = f16x2_of_e4m3x2(b);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+        x[k][2 * i] = (x[k][2 * i] - f.x) * 16.0f;
+        x[k][2 * i + 1] = (x[k][2 * i + 1] - f.y) * 16.0f;
+      }
+      const uint32_t at = smem + C::kOffQ + buf * C::kQBytes + tc::swz(d * C::NC + c, lane * kPer, C::kHD);
+      if constexpr (kPer == 4) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(word) : "memory");
+      else asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)word) : "memory");
+    }
+    if (lane == 0) {
+      const float per = a.sm_scale * __uint_as_float((uint32_t)(127 + e - 7) << 23);
+      auto& col = sh.col[buf][c];
+      col.qscale = C::CAP ? per / a.softcap : per * kLog2e;
+      const int64_t hi = (int64_t)p.pos0 + qi[k] + 1, lo = a.window > 0 ? hi - a.window : 0;
+      col.hi = qi[k] < 0 || hi < 0 ? 0 : (hi < p.cap ? (int)hi : p.cap);
+      col.lo = lo < 0 ? 0 : (lo < 0x7FFFFFFF ? (int)lo : 0x7FFFFFFF);
+      col.row = qi[k] < 0 ? -1 : (p.q0 + i0 + qi[k]) * a.Hq + p.head0 + hd[k];
+    }
+  }
+  tc::fence_async_smem();
+  __syncwarp();
+  if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.qfull[buf]));
+  return true;
+}
 
 // ---- producer --------------------------------------------------------------------------
 template <class C>
@@ -147,8 +288,10 @@ __device__ void produce(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, ui
   uint32_t bad = 0;
   int64_t nk = 0, nv = 0;  // tiles of K and of V whose copies were issued
   bool ok = true;
+  uint32_t piece = 0;
   Walk w;
-  for (w.start(a, s, sh.share); ok && w.left > 0; w.next(a, s)) {
+  if (lane == 0) a.meta[(int64_t)blockIdx.x * kMetaInts] = 0;
+  for (w.start(a, s, sh.share); ok && w.left > 0; w.next(a, s), ++piece) {
     const int h = w.hh / s.nhb;
     const int32_t* row = a.table + (int64_t)w.r * a.max_pages;
     const int p_end = (w.g.hi + page - 1) >> a.page_log2, p_beg = w.g.lo >> a.page_log2;
@@ -170,8 +313,7 @@ __device__ void produce(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, ui
       const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, valid)) * page_bytes;
       const int st = (int)(nk % C::kStages);
       const uint32_t parity = (uint32_t)(nk / C::kStages + 1) & 1u;
-      const int64_t head = (int64_t)id * a.Hk + h;
-      const int at = (int)(head << a.page_log2);
+      const int head = id * a.Hk + h, at = head << a.page_log2;  // rows of a cache are below 2^31
       ok = __all_sync(0xffffffffu, kv_wait(&sh.abort, sh.kempty[st], parity));
       if (!ok) break;
       const uint32_t kb = tc::smem_u32(&sh.kfull[st]);
@@ -197,6 +339,11 @@ __device__ void produce(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, ui
         tc::mbar_arrive(vb);
       }
       ++nv;
+      if (i == 0) {  // behind the first tile's copies
+        ok = kv_wait_all(sh, sh.qfree[piece & 1u], ((piece >> 1) & 1u) ^ 1u);
+        if (!ok) break;
+        fetch_queries<C>(a, s, sh, smem, w, (int)(piece & 1u));
+      }
     }
   }
   if (!ok) {  // given up: no copy may land after the CTA has gone
@@ -210,28 +357,27 @@ __device__ void produce(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, ui
 
 // ---- products (one warp) ----------------------------------------------------------------
 template <class C>
-__device__ void multiply(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uint32_t smem, uint32_t tmem) {
+__device__ void multiply(KvShared<C>& sh, uint32_t smem, uint32_t tmem) {
   constexpr uint32_t kIdS = idesc_e4m3(kKeys, C::NS, false, false);
   constexpr uint32_t kIdO = idesc_e4m3(128, C::NP, true, true);
   // K tile and queries: rows of HD bytes, K-major.  V tile: the same bytes read MN-major (with
   // 64 channels the second half of the 128 M rows repeats the first: leading offset 0).  P:
   // granules of 16 columns x 128 keys, 16 bytes per key, MN-major, no swizzle.
   const uint64_t dk0 = tc::smem_desc(smem + C::kOffK, 16, 8 * C::kHD, C::kSwz);
-  const uint64_t dq = tc::smem_desc(smem + C::kOffQ, 16, 8 * C::kHD, C::kSwz);
+  const uint64_t dq0 = tc::smem_desc(smem + C::kOffQ, 16, 8 * C::kHD, C::kSwz);
   const uint64_t dv0 = tc::smem_desc(smem + C::kOffV, 0, 8 * C::kHD, C::kSwz);
   const uint64_t dp = tc::smem_desc(smem + C::kOffP, 128, 16 * kKeys, 0);
   int64_t n = 0;
   uint32_t piece = 0;
   const bool on = (threadIdx.x & 31) == 0;
   bool ok = true;
-  Walk w;
   auto scores = [&](int64_t m) {  // S of tile m
     const int st = (int)(m % C::kStages);
     ok = kv_wait_all(sh, sh.kfull[st], (uint32_t)(m / C::kStages) & 1u) &&
          kv_wait_all(sh, sh.sfree[m & 1], ((uint32_t)(m >> 1) & 1u) ^ 1u);
     if (!ok) return;
     tc::fence_after_sync();
-    const uint64_t dk = tc::desc_add(dk0, st * C::kTile);
+    const uint64_t dk = tc::desc_add(dk0, st * C::kTile), dq = tc::desc_add(dq0, (piece & 1u) * C::kQBytes);
     const uint32_t d = tmem + C::kColS + (uint32_t)(m & 1) * C::NS;
 #pragma unroll
     for (int k = 0; k < C::kHD / 32; ++k)
@@ -239,12 +385,14 @@ __device__ void multiply(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, u
     commit_if(on, tc::smem_u32(&sh.sfull[m & 1]));
     commit_if(on, tc::smem_u32(&sh.kempty[st]));
   };
-  for (w.start(a, s, sh.share); ok && w.left > 0; w.next(a, s), ++piece) {
-    ok = kv_wait_all(sh, sh.qfull, piece & 1u);
+  int take = 0;
+  for (int64_t left = uniform(sh.share.left); ok && left > 0; left -= take, ++piece) {
+    ok = kv_wait_all(sh, sh.qfull[piece & 1u], (piece >> 1) & 1u);
     if (!ok) break;
+    take = uniform(sh.piece[piece & 1u].take);
     scores(n);
-    for (int i = 0; ok && i < w.take; ++i, ++n) {
-      if (i + 1 < w.take) scores(n + 1);
+    for (int i = 0; ok && i < take; ++i, ++n) {
+      if (i + 1 < take) scores(n + 1);
       const int st = (int)(n % C::kStages);
       ok = ok && kv_wait_all(sh, sh.vfull[st], (uint32_t)(n / C::kStages) & 1u) &&
            kv_wait_all(sh, sh.pfull, (uint32_t)n & 1u);
@@ -266,121 +414,40 @@ __device__ void multiply(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, u
 }
 
 // ---- softmax -----------------------------------------------------------------------------
-// Query rows of the piece as E4M3 digits (row d * NC + column of the Q operand), and what each
-// column needs later.
-template <class C, typename T>
-__device__ __forceinline__ void load_queries(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uint32_t smem,
-                                             const Walk& w) {
-  constexpr int kWarps = C::kSoft / 32, kPer = C::kHD / 32;  // elements per lane
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = w.hh / s.nhb, hb = w.hh % s.nhb;
-  const int nh = s.G - hb * s.HB < s.HB ? s.G - hb * s.HB : s.HB;  // heads in this block
-#pragma unroll 4
-  for (int c = warp; c < C::NC; c += kWarps) {
-    const int qi = c / s.HB, hd = c - qi * s.HB;
-    const int i = w.qb * s.QB + qi;
-    const bool live = qi < s.QB && i < w.x.n && hd < nh;
-    const int head = h * s.G + hb * s.HB + hd;
-    uint32_t raw[kPer / 2];
-#pragma unroll
-    for (int k = 0; k < kPer / 2; ++k) raw[k] = 0;
-    if (live) {
-      const uint8_t* p = a.q + (int64_t)(w.x.q0 + i) * a.q_stride + (int64_t)head * (C::kHD * 2) + lane * (kPer * 2);
-      if constexpr (kPer == 4) {
-        const uint2 v = *reinterpret_cast<const uint2*>(p);
-        raw[0] = v.x;
-        raw[1] = v.y;
-      } else {
-        raw[0] = *reinterpret_cast<const uint32_t*>(p);
-      }
-    }
-    float x[kPer];
-    float amax = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kPer / 2; ++k) {
-      if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&raw[k]));
-        x[2 * k] = f.x;
-        x[2 * k + 1] = f.y;
-      } else {
-        x[2 * k] = bf16_lo(raw[k]);
-        x[2 * k + 1] = bf16_hi(raw[k]);
-      }
-      amax = fmaxf(amax, fmaxf(fabsf(x[2 * k]), fabsf(x[2 * k + 1])));
-    }
-    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-    int e = (int)(__float_as_uint(amax) >> 23) - 127;  // amax in [2^e, 2^(e+1))
-    e = e < -100 ? -100 : e;
-    const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) x[k] *= up;
-#pragma unroll
-    for (int d = 0; d < C::DQ; ++d) {
-      uint32_t word = 0;
-#pragma unroll
-      for (int k = 0; k < kPer / 2; ++k) {
-        const uint32_t b = e4m3x2_sat(x[2 * k], x[2 * k + 1]);
-        word |= b << (16 * k);
-        const uint32_t back = f16x2_of_e4m3x2(b);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
-        x[2 * k] = (x[2 * k] - f.x) * 16.0f;
-        x[2 * k + 1] = (x[2 * k + 1] - f.y) * 16.0f;
-      }
-      const uint32_t at = smem + C::kOffQ + tc::swz(d * C::NC + c, lane * kPer, C::kHD);
-      if constexpr (kPer == 4) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(word) : "memory");
-      else asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)word) : "memory");
-    }
-    if (lane == 0) {
-      const float per = a.sm_scale * __uint_as_float((uint32_t)(127 + e - 7) << 23);
-      sh.qscale[c] = C::CAP ? per / a.softcap : per * kLog2e;
-      const int64_t pos = (int64_t)w.x.pos0 + i;
-      const int64_t hi = pos + 1, lo = a.window > 0 ? pos + 1 - a.window : 0;
-      sh.col_hi[c] = !live || hi < 0 ? 0 : (hi < w.x.cap ? (int)hi : w.x.cap);
-      sh.col_lo[c] = lo < 0 ? 0 : (lo < 0x7FFFFFFF ? (int)lo : 0x7FFFFFFF);
-      sh.col_row[c] = live ? (int64_t)(w.x.q0 + i) * a.Hq + head : -1;
-    }
-  }
-}
-
 template <class C, typename T>
 __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uint8_t* smem_p, uint32_t tmem) {
-  constexpr int CW = C::CW;
+  constexpr int CW = C::NC;
   const uint32_t smem = tc::smem_u32(smem_p);
-  const int tid = threadIdx.x, lane = tid & 31, wg = tid >> 7, wq = (tid >> 5) & 3, row = tid & 127;
-  const int bar = 1 + wg;
-  const int c0 = wg * CW;
+  const int tid = threadIdx.x, lane = tid & 31, wq = tid >> 5, row = tid;
   const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
   const float cap2 = C::CAP ? a.softcap * kLog2e : 0.0f;
-  if (tid == 0) a.meta[(int64_t)blockIdx.x * kMetaInts] = 0;
   bool bad = false;
   int64_t n = 0;
-  Walk w;
-  for (w.start(a, s, sh.share); w.left > 0; w.next(a, s)) {
-    load_queries<C, T>(a, s, sh, smem, w);
-    tc::fence_async_smem();
-    asm volatile("bar.sync 3, %0;" ::"n"(C::kSoft) : "memory");  // columns known to every softmax thread
-    tc::mbar_arrive(tc::smem_u32(&sh.qfull));
+  uint32_t piece = 0;
+  int take;
+  if (sh.share.left > 0) bad = !prepare_queries<C, T>(a, s, sh, smem, 0);
+  if (tc::named_sync_or(1, 128, bad)) return;  // the columns are known to every softmax thread
+  for (int64_t left = sh.share.left; left > 0; left -= take, ++piece) {
+    const int buf = (int)(piece & 1u);
+    const auto& w = sh.piece[buf];
+    take = w.take;
+    const int lo = w.lo, hi = w.hi, all_lo = w.all_lo, all_hi = w.all_hi, tile = w.tile;
     float qs[CW], m[CW], l[CW];
 #pragma unroll
     for (int c = 0; c < CW; ++c) {
-      qs[c] = sh.qscale[c0 + c];
+      qs[c] = sh.col[buf][c].qscale;
       m[c] = 0.0f;
       l[c] = 0.0f;
     }
     uint32_t unseen = 0xffffffffu >> (32 - CW);  // columns that have seen no key yet
-    // keys that every live column sees: the block's first query ends soonest, its last starts latest
-    const int last_q = (w.qb + 1) * s.QB < w.x.n ? (w.qb + 1) * s.QB - 1 : w.x.n - 1;
-    const int64_t all_hi64 = (int64_t)w.x.pos0 + w.qb * s.QB + 1;
-    const int all_hi = all_hi64 < 0 ? 0 : (all_hi64 < w.x.cap ? (int)all_hi64 : w.x.cap);
-    const int64_t all_lo64 = a.window > 0 ? (int64_t)w.x.pos0 + last_q + 1 - a.window : 0;
-    for (int i = 0; i < w.take; ++i, ++n) {
+    for (int i = 0; i < take; ++i, ++n) {
       const int st = (int)(n % C::kStages);
       bad |= !kv_wait(&sh.abort, sh.sfull[n & 1], (uint32_t)(n >> 1) & 1u);
       bad |= !kv_wait(&sh.abort, sh.vfull[st], (uint32_t)(n / C::kStages) & 1u);
       tc::fence_after_sync();
       float u[CW];
       {
-        const uint32_t at = lanes + C::kColS + (uint32_t)(n & 1) * C::NS + c0;
+        const uint32_t at = lanes + C::kColS + (uint32_t)(n & 1) * C::NS;
         uint32_t d[CW];
         tmem_ld<CW>(at, d);
 #pragma unroll
@@ -395,11 +462,12 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
         }
       }
       tc::fence_before_sync();
-      tc::mbar_arrive(tc::smem_u32(&sh.sfree[n & 1]));
-      const int key0 = (w.g.tile + w.off + i) * kKeys, key = key0 + row;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.sfree[n & 1]));
+      const int key0 = (tile + i) * kKeys, key = key0 + row;
       const float ks = sh.ks[st][row >> a.page_log2];
       float vs = sh.vs[st][row >> a.page_log2];
-      const bool there = vs >= 0.0f && key >= w.g.lo && key < w.g.hi;
+      const bool there = vs >= 0.0f && key >= lo && key < hi;
       vs = fmaxf(vs, 5.421010862427522e-20f);  // 2^-64
       const float lv = __log2f(vs), per_v = __fdividef(1.0f, vs);
       if constexpr (C::CAP) {
@@ -416,10 +484,10 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
       if (!there) {
 #pragma unroll
         for (int c = 0; c < CW; ++c) u[c] = -INFINITY;
-      } else if (key0 + kKeys > all_hi || key0 < all_lo64) {
+      } else if (key0 + kKeys > all_hi || key0 < all_lo) {
 #pragma unroll
         for (int c = 0; c < CW; ++c)
-          if (key >= sh.col_hi[c0 + c] || key < sh.col_lo[c0 + c]) u[c] = -INFINITY;
+          if (key >= sh.col[buf][c].hi || key < sh.col[buf][c].lo) u[c] = -INFINITY;
       }
       bool exceed = false;
 #pragma unroll
@@ -428,8 +496,8 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
 #pragma unroll
         for (int c = 0; c < CW; ++c) exceed |= ((unseen >> c) & 1u) && u[c] > -INFINITY;
       }
-      if (tc::named_sync_or(bar, 128, exceed || bad)) {
-        if (tc::named_sync_or(bar, 128, bad)) {
+      if (tc::named_sync_or(1, 128, exceed || bad)) {
+        if (tc::named_sync_or(1, 128, bad)) {
           bad = true;
           break;
         }
@@ -437,14 +505,14 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
 #pragma unroll
         for (int c = 0; c < CW; ++c) t[c] = u[c];
         const float top = warp_columns<CW, true>(t, lane);
-        if (lane < CW) sh.red[wg][wq][lane] = top;
-        asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
+        if (lane < CW) sh.red[wq][lane] = top;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
         if (i > 0) bad |= !kv_wait(&sh.abort, sh.pvdone, (uint32_t)(n - 1) & 1u);
         tc::fence_after_sync();
         float f[CW];
 #pragma unroll
         for (int c = 0; c < CW; ++c) {
-          const float mx = fmaxf(fmaxf(sh.red[wg][0][c], sh.red[wg][1][c]), fmaxf(sh.red[wg][2][c], sh.red[wg][3][c]));
+          const float mx = fmaxf(fmaxf(sh.red[0][c], sh.red[1][c]), fmaxf(sh.red[2][c], sh.red[3][c]));
           const bool fresh = (unseen >> c) & 1u;
           const float up = mx == -INFINITY ? 0.0f : (fresh ? mx : (mx > kSlack ? mx : 0.0f));
           if (fresh && mx != -INFINITY) unseen &= ~(1u << c);
@@ -457,14 +525,14 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
 #pragma unroll
           for (int d = 0; d < 3; ++d) {
             uint32_t o[CW];
-            tmem_ld<CW>(lanes + C::kColO + d * C::NC + c0, o);
+            tmem_ld<CW>(lanes + C::kColO + d * C::NC, o);
 #pragma unroll
             for (int c = 0; c < CW; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f[c]);
-            tmem_st<CW>(lanes + C::kColO + d * C::NC + c0, o);
+            tmem_st<CW>(lanes + C::kColO + d * C::NC, o);
           }
           tc::tmem_wait_st();
         }
-        asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");  // red may be written again
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // red may be written again
       } else if (i > 0) {
         bad |= !kv_wait(&sh.abort, sh.pvdone, (uint32_t)(n - 1) & 1u);  // P may be written again
       }
@@ -490,7 +558,7 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
       }
 #pragma unroll
       for (int d = 0; d < 3; ++d) {
-        const int col = d * C::NC + c0;
+        const int col = d * C::NC;
         const uint32_t at = smem + C::kOffP + (col / 16) * (16 * kKeys) + row * 16 + col % 16;
         if constexpr (CW == 8) {
           asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(dig[d][0]), "r"(dig[d][1]) : "memory");
@@ -501,50 +569,52 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
                              make_uint4(dig[d][4 * k], dig[d][4 * k + 1], dig[d][4 * k + 2], dig[d][4 * k + 3]));
         }
       }
-      if (!there && wg == 0) {  // whatever lies there (NaN included) times a zero probability
+      if (!there) {  // whatever lies there (NaN included) times a zero probability
 #pragma unroll
         for (int k = 0; k < C::kHD / 16; ++k)
           tc::st_shared_v4(smem + C::kOffV + st * C::kTile + row * C::kHD + k * 16, make_uint4(0u, 0u, 0u, 0u));
       }
       tc::fence_async_smem();
       tc::fence_before_sync();
-      tc::mbar_arrive(tc::smem_u32(&sh.pfull));
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.pfull));
     }
+    if (!bad && left > take) bad = !prepare_queries<C, T>(a, s, sh, smem, piece + 1);
     if (!bad) bad = !kv_wait(&sh.abort, sh.pvdone, (uint32_t)(n - 1) & 1u);
-    if (tc::named_sync_or(3, C::kSoft, bad)) break;
+    if (tc::named_sync_or(1, 128, bad)) break;
     tc::fence_after_sync();
     // sums over the keys: the warp's rows, then the four warps
     const float sum = warp_columns<CW, false>(l, lane);
-    if (lane < CW) sh.red[wg][wq][lane] = sum;
-    asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
-    const bool whole = w.first && w.last;
+    if (lane < CW) sh.red[wq][lane] = sum;
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    const bool whole = w.whole != 0;
     const int slot = w.first ? 1 : 0;
     float* part = a.part + ((int64_t)blockIdx.x * 2 + slot) * (C::NC * (C::kHD + 2));
     if (row < CW) {
-      const float tot = (sh.red[wg][0][row] + sh.red[wg][1][row]) + (sh.red[wg][2][row] + sh.red[wg][3][row]);
+      const float tot = (sh.red[0][row] + sh.red[1][row]) + (sh.red[2][row] + sh.red[3][row]);
       float mm = 0.0f;
 #pragma unroll
       for (int c = 0; c < CW; ++c) mm = row == c ? m[c] : mm;
-      const int64_t to = sh.col_row[c0 + row];
+      const int to = sh.col[buf][row].row;
       if (whole) {
-        sh.linv[c0 + row] = tot != 0.0f ? __fdiv_rn(1.0f, tot) : 0.0f;
+        sh.linv[row] = tot != 0.0f ? __fdiv_rn(1.0f, tot) : 0.0f;
         if (a.lse && to >= 0) a.lse[to] = tot != 0.0f ? (mm + log2f(tot) - kLift) * kLn2 : -INFINITY;
       } else {
-        part[C::NC * C::kHD + 2 * (c0 + row)] = mm;
-        part[C::NC * C::kHD + 2 * (c0 + row) + 1] = tot;
+        part[C::NC * C::kHD + 2 * (row)] = mm;
+        part[C::NC * C::kHD + 2 * (row) + 1] = tot;
       }
     }
-    asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
+    asm volatile("bar.sync 1, 128;" ::: "memory");
     {
       float o[CW];
       uint32_t d[CW];
-      tmem_ld<CW>(lanes + C::kColO + c0, d);
+      tmem_ld<CW>(lanes + C::kColO, d);
 #pragma unroll
       for (int c = 0; c < CW; ++c) o[c] = __uint_as_float(d[c]);
-      tmem_ld<CW>(lanes + C::kColO + C::NC + c0, d);
+      tmem_ld<CW>(lanes + C::kColO + C::NC, d);
 #pragma unroll
       for (int c = 0; c < CW; ++c) o[c] = fmaf(__uint_as_float(d[c]), 0.0625f, o[c]);
-      tmem_ld<CW>(lanes + C::kColO + 2 * C::NC + c0, d);
+      tmem_ld<CW>(lanes + C::kColO + 2 * C::NC, d);
 #pragma unroll
       for (int c = 0; c < CW; ++c) o[c] = fmaf(__uint_as_float(d[c]), 0.00390625f, o[c]);
       if (row < C::kHD) {
@@ -552,25 +622,23 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
           T* out = reinterpret_cast<T*>(a.out);
 #pragma unroll
           for (int c = 0; c < CW; ++c) {
-            const int64_t to = sh.col_row[c0 + c];
-            if (to >= 0) out[to * C::kHD + row] = from_float<T>(o[c] * sh.linv[c0 + c]);
+            const int to = sh.col[buf][c].row;
+            if (to >= 0) out[(int64_t)to * C::kHD + row] = from_float<T>(o[c] * sh.linv[c]);
           }
         } else {
 #pragma unroll
-          for (int c = 0; c < CW; ++c) part[(c0 + c) * C::kHD + row] = o[c];
+          for (int c = 0; c < CW; ++c) part[(c) * C::kHD + row] = o[c];
         }
       }
     }
     tc::fence_before_sync();
-    if (!whole && w.first && tid == 0) note_item(a, sh.share, w);
-    // the next piece's queries may replace these: every product of this one has completed, and
-    // every softmax thread has read its columns
-    asm volatile("bar.sync 3, %0;" ::"n"(C::kSoft) : "memory");
+    asm volatile("bar.sync 1, 128;" ::: "memory");  // every thread is done with red, linv and the columns
+    if (tid == 0) tc::mbar_arrive(tc::smem_u32(&sh.qfree[buf]));
   }
 }
 
 template <class C, typename T>
-__global__ void __launch_bounds__(C::kThreads) kv8_attn_kernel(const __grid_constant__ CUtensorMap kmap,
+__global__ void __launch_bounds__(C::kThreads, C::kCtas) kv8_attn_kernel(const __grid_constant__ CUtensorMap kmap,
                                                                 const __grid_constant__ CUtensorMap vmap,
                                                                 const KvAttnArgs a) {
   extern __shared__ uint8_t raw[];
@@ -586,10 +654,12 @@ __global__ void __launch_bounds__(C::kThreads) kv8_attn_kernel(const __grid_cons
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(tc::smem_u32(&sh.sfull[i]), 1);
-      tc::mbar_init(tc::smem_u32(&sh.sfree[i]), C::kSoft);
+      tc::mbar_init(tc::smem_u32(&sh.sfree[i]), 4);
+      tc::mbar_init(tc::smem_u32(&sh.rows[i]), 33);
+      tc::mbar_init(tc::smem_u32(&sh.qfull[i]), 4);
+      tc::mbar_init(tc::smem_u32(&sh.qfree[i]), 1);
     }
-    tc::mbar_init(tc::smem_u32(&sh.qfull), C::kSoft);
-    tc::mbar_init(tc::smem_u32(&sh.pfull), C::kSoft);
+    tc::mbar_init(tc::smem_u32(&sh.pfull), 4);
     tc::mbar_init(tc::smem_u32(&sh.pvdone), 1);
     tc::mbar_init(tc::smem_u32(&sh.drain), 1);
     sh.abort = 0;
@@ -613,7 +683,7 @@ __global__ void __launch_bounds__(C::kThreads) kv8_attn_kernel(const __grid_cons
   } else if (warp == C::kSoft / 32) {
     produce<C>(a, s, sh, tc::smem_u32(smem), &kmap, &vmap);
   } else {
-    multiply<C>(a, s, sh, tc::smem_u32(smem), tmem);
+    multiply<C>(sh, tc::smem_u32(smem), tmem);
   }
   __syncwarp();
   tc::fence_before_sync();

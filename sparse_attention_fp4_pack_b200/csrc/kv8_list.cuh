@@ -283,18 +283,32 @@ struct Walk {
   }
 };
 
+// a / b of nonnegative numbers, which mostly fit 32 bits (64-bit divisions take far longer).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// Sum of the lanes' values up to and including this one's.
+__device__ __forceinline__ int64_t warp_upto(int64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
 // First tile of CTA c's share.  With fewer tiles than CTAs the first CTAs take one each, so the
 // pieces of an item are always neighbours.
 __device__ __forceinline__ int64_t share_ctas(int64_t total) { return total < gridDim.x ? total : gridDim.x; }
 __device__ __forceinline__ int64_t share_start(int64_t total, int64_t c) {
   const int64_t C = share_ctas(total);
-  return c < C ? total * c / C : total;  // at most 2^31 items of 2^23 tiles: below 2^63
+  return c < C ? quotient(total * c, C) : total;  // at most 2^31 items of 2^23 tiles: below 2^63
 }
 // Notes the item that this CTA starts with `w` and does not end.
 __device__ __forceinline__ void note_item(const KvAttnArgs& a, const Share& share, const Walk& w) {
   const int64_t last = share_start(share.total, blockIdx.x + 1) + (w.g.tiles - w.off - w.take) - 1;  // its last tile
   // the largest c with total * c / C <= last
-  const int c = (int)(((last + 1) * share_ctas(share.total) - 1) / share.total);
+  const int c = (int)quotient((last + 1) * share_ctas(share.total) - 1, share.total);
   int32_t* meta = a.meta + (int64_t)blockIdx.x * kMetaInts;
   meta[0] = 1;
   meta[1] = c;
@@ -304,10 +318,11 @@ __device__ __forceinline__ void note_item(const KvAttnArgs& a, const Share& shar
   meta[5] = w.x.n;
 }
 
-// Computed by the whole CTA (kThreads threads); `sums` holds a value per thread.
+// Computed by the whole CTA (kThreads threads); `sums` holds a value per warp.
 template <int kThreads>
 __device__ void find_share(const KvAttnArgs& a, const Shape& s, int64_t* sums, Share* out, uint32_t* bad) {
-  const int tid = threadIdx.x, lane = tid & 31;
+  constexpr int kWarps = kThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.R + kThreads - 1) / kThreads;  // requests per thread, consecutive
   const int heads = a.Hk * s.nhb;
   int64_t mine = 0;
@@ -315,82 +330,69 @@ __device__ void find_share(const KvAttnArgs& a, const Shape& s, int64_t* sums, S
     const int r = tid * per + i;
     mine += lane_row_tiles(a, s, r, r < a.R, lane, bad);
   }
-  sums[tid] = mine * heads;
+  mine *= heads;
+  int64_t upto = warp_upto(mine, lane);
+  if (lane == 31) sums[warp] = upto;
   __syncthreads();
-  if (tid < 32) {
-    constexpr int kEach = kThreads / 32;
-    int64_t part = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) part += sums[lane * kEach + i];
-    int64_t upto = part;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += y;
-    }
-    const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
-    const int64_t t0 = share_start(total, blockIdx.x), t1 = share_start(total, blockIdx.x + 1);
-    Share w = {t1 - t0, t0, total, 0, 0, 0, 0};
-    if (w.left > 0) {
-      // the thread whose requests hold tile t0 ...
-      const unsigned m = __ballot_sync(0xffffffffu, upto > t0);
-      const int l0 = __ffs(m) - 1;
-      int64_t before = __shfl_sync(0xffffffffu, upto - part, l0);
-      int th = l0 * kEach;
-      while (before + sums[th] <= t0) before += sums[th++];
-      // ... the request (32 at a time) ...
-      int64_t rest = t0 - before;
-      int r = th * per;
-      Request x;
-      int64_t row;
+  const int64_t of_warps = warp_upto(lane < kWarps ? sums[lane] : 0, lane);
+  const int64_t total = __shfl_sync(0xffffffffu, of_warps, kWarps - 1);
+  const int64_t warps_before = __shfl_sync(0xffffffffu, of_warps, warp > 0 ? warp - 1 : 0);
+  if (warp > 0) upto += warps_before;
+  const int64_t t0 = share_start(total, blockIdx.x), left = share_start(total, blockIdx.x + 1) - t0;
+  if (tid == 0) {
+    out->left = left;
+    out->t0 = t0;
+    out->total = total;
+  }
+  // the thread whose requests hold tile t0: its warp finds the request (32 at a time) ...
+  const unsigned holder = __ballot_sync(0xffffffffu, left > 0 && upto - mine <= t0 && t0 < upto);
+  if (holder) {
+    const int src = __ffs(holder) - 1;
+    int64_t rest = t0 - __shfl_sync(0xffffffffu, upto - mine, src), row = __shfl_sync(0xffffffffu, mine, src);
+    int r = (warp * 32 + src) * per;
+    if (per > 1) {
       for (;;) {
-        const int64_t n = lane_row_tiles(a, s, r + lane, r + lane < a.R, lane, bad) * heads;
-        int64_t in = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, in, o);
-          if (lane >= o) in += y;
-        }
+        const int64_t n = lane_row_tiles(a, s, r + lane, r + lane < a.R, lane, bad) * heads, in = warp_upto(n, lane);
         const unsigned hit = __ballot_sync(0xffffffffu, in > rest);
         if (hit) {
           const int l = __ffs(hit) - 1;
           rest -= __shfl_sync(0xffffffffu, in - n, l);
-          row = __shfl_sync(0xffffffffu, n, l) / heads;
+          row = __shfl_sync(0xffffffffu, n, l);
           r += l;
           break;
         }
         rest -= __shfl_sync(0xffffffffu, in, 31);
         r += 32;
       }
-      x = request_of(a, s, r, bad);
-      w.r = r;
-      w.hh = (int)(rest / row);
-      rest -= (int64_t)w.hh * row;
-      // ... and the query block
-      for (int qb0 = 0;; qb0 += 32) {
-        const int n = qb0 + lane < x.nqb ? range_of(a, s, x, qb0 + lane).tiles : 0;
-        int64_t in = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, in, o);
-          if (lane >= o) in += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, in > rest);
-        if (hit) {
-          const int l = __ffs(hit) - 1;
-          w.qb = qb0 + l;
-          w.off = (int)(rest - __shfl_sync(0xffffffffu, in - n, l));
-          break;
-        }
-        rest -= __shfl_sync(0xffffffffu, in, 31);
-        if (qb0 + 32 >= x.nqb) break;  // cannot happen
-      }
     }
-    if (lane == 0) *out = w;
+    row = quotient(row, heads);
+    const Request x = request_of(a, s, r, bad);
+    const int hh = (int)quotient(rest, row);
+    rest -= (int64_t)hh * row;
+    // ... and the query block
+    int qb = 0;
+    while (x.nqb > 1) {
+      const int64_t n = qb + lane < x.nqb ? range_of(a, s, x, qb + lane).tiles : 0, in = warp_upto(n, lane);
+      const unsigned hit = __ballot_sync(0xffffffffu, in > rest);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        rest -= __shfl_sync(0xffffffffu, in - n, l);
+        qb += l;
+        break;
+      }
+      rest -= __shfl_sync(0xffffffffu, in, 31);
+      qb += 32;
+      if (qb >= x.nqb) break;  // cannot happen
+    }
+    if (lane == 0) {
+      out->r = r;
+      out->hh = hh;
+      out->qb = qb;
+      out->off = (int)rest;
+    }
   }
   __syncthreads();
 }
-
 
 // Joins the pieces of the item that CTA blockIdx.x starts and does not end: with M the largest
 // of the pieces' maxima, out = sum 2^(m - M) O / sum 2^(m - M) l.  A warp joins one column: its
