@@ -380,8 +380,10 @@ csa2_status csa2_paged_release(const int32_t* seq_len, const int32_t* block_tabl
  * max(page's scale, s_new).  Rows before the first written one are re-encoded when s grew:
  * code' = E4M3_RNE(code * (old / s)) (a power of two: exact but for subnormal codes).  New
  * rows: code = E4M3_RNE_sat(x / s).  A power of two costs E4M3 no precision, and a page may be
- * re-scaled any number of times without the rounding adding up.  Output is bit-exact with that
- * definition.  Slots outside [-1, n_pages*page) and rows that break the order within their
+ * re-scaled any number of times without the rounding adding up.  A NaN is stored as NaN and
+ * counts for nothing in s_new; an infinity counts as the largest magnitude (s_new = 2^120) and
+ * is stored as 448.  Output is bit-exact with that definition.  Slots outside
+ * [-1, n_pages*page) and rows that do not follow their neighbour in the same
  * page are skipped and flag CSA2_DEV_BAD_INDEX. */
 csa2_status csa2_kv8_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, int dtype, int64_t T,
                             int Hk, int hd, const int64_t* slot_map, uint8_t* k_cache, uint8_t* v_cache,
@@ -398,16 +400,21 @@ csa2_status csa2_kv8_append(const void* k, const void* v, int64_t k_stride, int6
  *   softcap > 0: scores s become softcap * tanh(s / softcap); 0 leaves them
  *   out 16-bit [T][Hq][hd];  lse fp32 [T][Hq] (natural log; may be NULL)
  * s = sm_scale * q . (k_scale K), out = softmax(s) (v_scale V).  Both products run on the
- * tcgen05 tensor cores on the E4M3 codes as stored; the queries enter as E4M3 digits that hold
- * every bf16 / fp16 value to 2^-22 of its head's largest element, the probabilities rounded to
- * f16; sums are fp32.  Scales: k_scale finite, v_scale in [0, 2^64].  A row that sees no key
- * gives out = 0, lse = -inf.  Rows of q outside every request are not read and theirs of out and
- * lse are left as they were; what the cache holds outside the rows a request sees (any bits,
- * NaN included) does not matter.  Entries of block_table outside [0, n_pages) among the pages a
- * request sees are masked and flag CSA2_DEV_BAD_INDEX; lengths that are negative, shorter than
- * the rows brought, or longer than the table, and q_start outside [0, T] or descending are cut
- * and flag CSA2_DEV_BAD_COUNT.  Results do not depend on timing: the same call gives the same
- * bits. */
+ * tcgen05 tensor cores.  Up to 16 rows per key head (max_q * Hq/Hk) they run on the E4M3 codes
+ * as stored; the queries enter as E4M3 digits that hold every bf16 / fp16 value to 2^-22 of its
+ * row's largest element.  Beyond that the codes enter as f16, which holds them exactly, and the
+ * queries as f16 to 2^-38 of that element.  The probabilities are rounded to f16; sums are fp32.
+ * Scales: k_scale of magnitude up to 2^100, v_scale in [0, 2^120].
+ * A row that sees no key gives out = 0, lse = -inf.  A NaN or an infinity in a query row gives
+ * NaN in that row alone; a NaN key code gives NaN in the rows that see it; a NaN value code may
+ * give NaN in any row of its request.  Rows of q outside every request are not read and theirs of
+ * out and lse are left as they were; what the cache holds outside the tokens a request sees (any
+ * bits, NaN included) does not matter.  Entries of block_table outside [0, n_pages) among the
+ * pages a request sees are masked and flag CSA2_DEV_BAD_INDEX; lengths that are negative, shorter
+ * than the rows brought, or longer than the table, and q_start outside [0, T] or descending are
+ * cut and flag CSA2_DEV_BAD_COUNT.  Requests' rows may not overlap, nor out the inputs.  ws:
+ * csa2_kv8_attn_workspace_size bytes for these arguments, any contents, used by one call at a
+ * time.  Results do not depend on timing: the same call gives the same bits. */
 size_t csa2_kv8_attn_workspace_size(int Hq, int Hk, int hd, int max_q, int dtype);
 csa2_status csa2_kv8_attn(const void* q, int64_t q_stride, int dtype, int64_t T, int Hq, int Hk, int hd,
                           const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,

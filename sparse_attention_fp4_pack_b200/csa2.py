@@ -513,19 +513,19 @@ _KV_DTYPES = {_BF16: 0, _F16: 1}
 
 
 def _refuse(t, dtype, shape, name, dev):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    """The shape first: it is what the C entry points cannot check."""
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+        raise ValueError(f"{name} must be on the device of the first argument, got {t.device}")
     raise ValueError(f"{name} must be contiguous")
 
 
 def _arg(t, dtype, shape, name, dev):
-    """Raise unless t is a contiguous `dtype` tensor of exactly `shape` on cuda:`dev`; its address."""
+    """Raise unless t is a contiguous `dtype` tensor of exactly `shape` on device `dev` (-1: the
+    host, refused when everything else is right); its address."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         _refuse(t, dtype, shape, name, dev)
     return t.data_ptr()
@@ -554,11 +554,9 @@ def _flag_arg(dev_status, dev):
     return dev_status.data_ptr()
 
 
-def _cuda_dev(t, name):
-    dev = t.get_device()
+def _need_cuda(dev, name):
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return dev
 
 
 def _length(t, name):
@@ -578,6 +576,7 @@ def _table(t, R, dev):
 
 def _call_on(dev, stream, fn, *args):
     """fn(*args, stream) with cuda:`dev` current (the library launches on the current device)."""
+    _need_cuda(dev, "every tensor")
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(dev)
     elif stream.device_index != dev:
@@ -596,7 +595,7 @@ def csa2_paged_plan(ctx_len, new_len, block_table, free_pages, n_free, page, n_p
     free_pages i32 [F] with n_free i32 [1] valid -> seq_len i32 [R], n_free_out i32 [1],
     q_start i32 [R+1], slot_map and pos i64 [T_cap] (see include/csa2.h).  seq_len may be
     ctx_len and n_free_out may be n_free."""
-    dev = _cuda_dev(ctx_len, "ctx_len")
+    dev = ctx_len.get_device()
     R, F, T = _length(ctx_len, "ctx_len"), _length(free_pages, "free_pages"), _length(slot_map, "slot_map")
     ta, cols = _table(block_table, R, dev)
     _check(_call_on(
@@ -613,7 +612,7 @@ def csa2_paged_release(seq_len, block_table, release, free_pages, n_free, page, 
     """The pages of requests whose release u8 [R] is nonzero, pushed onto free_pages i32 [F]
     after its n_free i32 [1] entries; seq_len_out i32 [R] (0 for those) and n_free_out i32 [1]
     may be seq_len and n_free."""
-    dev = _cuda_dev(seq_len, "seq_len")
+    dev = seq_len.get_device()
     R, F = _length(seq_len, "seq_len"), _length(free_pages, "free_pages")
     ta, cols = _table(block_table, R, dev)
     _check(_call_on(
@@ -637,7 +636,7 @@ def csa2_kv8_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, dev_stat
     """k, v bf16 or fp16 [T,Hk,hd] (token-strided views allowed) written as E4M3 codes into
     k_cache, v_cache u8 [n_pages,Hk,page,hd] at slot_map i64 [T], with one power-of-two scale
     per page and head in k_scale, v_scale f32 [n_pages,Hk] (see include/csa2.h)."""
-    dev = _cuda_dev(k, "k")
+    dev = k.get_device()
     (P, Hk, page, hd), cache = _cache_args(k_cache, v_cache, k_scale, v_scale, dev)
     dtype = k.dtype
     if dtype not in _KV_DTYPES:
@@ -667,7 +666,7 @@ def csa2_kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, q_start, s
     """q bf16 or fp16 [T,Hq,hd] (token-strided views allowed), the cache of csa2_kv8_append,
     block_table i32 [R,max_pages], q_start i32 [R+1], seq_len i32 [R] -> out like q
     (contiguous) and lse f32 [T,Hq] or None (see include/csa2.h)."""
-    dev = _cuda_dev(q, "q")
+    dev = q.get_device()
     (P, Hk, page, hd), cache = _cache_args(k_cache, v_cache, k_scale, v_scale, dev)
     dtype, sh = q.dtype, q.shape
     if dtype not in _KV_DTYPES:
@@ -678,7 +677,11 @@ def csa2_kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, q_start, s
     R, kind = _length(seq_len, "seq_len"), _KV_DTYPES[dtype]
     qa, qs = _tokens(q, dtype, sh, "q", dev)
     ta, cols = _table(block_table, R, dev)
+    qsa, sla = _arg(q_start, _I32, (R + 1,), "q_start", dev), _arg(seq_len, _I32, (R,), "seq_len", dev)
+    oa = _arg(out, dtype, (T, Hq, hd), "out", dev)
+    la = None if lse is None else _arg(lse, _F32, (T, Hq), "lse", dev)
     L = lib()
+    _need_cuda(dev, "q")
     if ws is None:
         # taken on the stream that uses it, so the allocator keeps it until the kernels are done
         need = _kv8_ws(dev, Hq, Hk, hd, max_q, kind)
@@ -691,7 +694,5 @@ def csa2_kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, q_start, s
         raise ValueError(f"ws must be a contiguous uint8 tensor on cuda:{dev}")
     _check(_call_on(
         dev, stream, L.csa2_kv8_attn, qa, qs, kind, T, Hq, Hk, hd, *cache, P, page, ta, cols,
-        _arg(q_start, _I32, (R + 1,), "q_start", dev), _arg(seq_len, _I32, (R,), "seq_len", dev), R,
-        max_q, sm_scale, window, softcap, _arg(out, dtype, (T, Hq, hd), "out", dev),
-        None if lse is None else _arg(lse, _F32, (T, Hq), "lse", dev), ws.data_ptr(), ws.numel(),
-        _flag_arg(dev_status, dev)), "csa2_kv8_attn")
+        qsa, sla, R, max_q, sm_scale, window, softcap, oa, la, ws.data_ptr(), ws.numel(), _flag_arg(dev_status, dev)),
+        "csa2_kv8_attn")

@@ -39,7 +39,6 @@
 
 namespace csa2 {
 
-constexpr int kMaxColumns = 32;
 constexpr float kLift = 6.0f;          // probabilities are 2^(t - max + 6), at most 2^8
 
 __host__ __device__ constexpr int round16(int n) { return (n + 15) / 16 * 16; }
@@ -56,8 +55,8 @@ struct KvCfg {
   static constexpr uint32_t kQBytes = (NS * HD + 1023) / 1024 * 1024;
   static constexpr uint32_t kPBytes = NP * kKeys;
   static constexpr uint32_t kRawBytes = NC * HD * 2;  // query rows as they come
-  static constexpr int kCtas = NC <= 16 ? 2 : 1;  // per SM
-  static constexpr uint32_t kBudget = (kCtas == 2 ? 112u : 224u) * 1024u - 4096u;
+  static constexpr int kCtas = 2;  // per SM
+  static constexpr uint32_t kBudget = 112u * 1024u - 4096u;
   static constexpr int kFit = (int)((kBudget - 2 * kQBytes - kPBytes - 2 * kRawBytes) / (2 * kTile));
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static constexpr uint32_t kOffK = 0, kOffV = kStages * kTile, kOffQ = 2 * kStages * kTile, kOffP = kOffQ + 2 * kQBytes;
@@ -75,15 +74,14 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool 
 }
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
+  static_assert(N == 8 || N == 16, "columns of a tile");
   if constexpr (N == 8) tc::tmem_ld8(addr, r);
-  else if constexpr (N == 16) tc::tmem_ld16(addr, r);
-  else tc::tmem_ld32(addr, r);
+  else tc::tmem_ld16(addr, r);
 }
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[N]) {
   if constexpr (N == 8) tc::tmem_st8_nowait(addr, r);
-  else if constexpr (N == 16) tc::tmem_st16_nowait(addr, r);
-  else tc::tmem_st32_nowait(addr, r);
+  else tc::tmem_st16_nowait(addr, r);
 }
 // N values per lane -> lane i holds value i mod N reduced over the warp (N - 1 exchanges, then
 // the remaining whole-warp ones).
@@ -265,7 +263,8 @@ __device__ __forceinline__ bool prepare_queries(const KvAttnArgs& a, const Shape
     if (lane == 0) {
       const float per = a.sm_scale * __uint_as_float((uint32_t)(127 + e - 7) << 23);
       auto& col = sh.col[buf][c];
-      col.qscale = C::CAP ? per / a.softcap : per * kLog2e;
+      // an infinite element leaves no digits of the others: the row's scores are NaN
+      col.qscale = isinf(amax[k]) ? __int_as_float(0x7FFFFFFF) : C::CAP ? per / a.softcap : per * kLog2e;
       const int64_t hi = (int64_t)p.pos0 + qi[k] + 1, lo = a.window > 0 ? hi - a.window : 0;
       col.hi = qi[k] < 0 || hi < 0 ? 0 : (hi < p.cap ? (int)hi : p.cap);
       col.lo = lo < 0 ? 0 : (lo < 0x7FFFFFFF ? (int)lo : 0x7FFFFFFF);
@@ -474,7 +473,7 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
         // cap * tanh(x), tanh(x) = 1 - 2 / (1 + e^2x): absolute error near 2^-23 of the cap
 #pragma unroll
         for (int c = 0; c < CW; ++c) {
-          const float e2 = exp2_approx(fminf(u[c] * ks * qs[c] * (2.0f * kLog2e), 126.0f));
+          const float x = u[c] * ks * qs[c] * (2.0f * kLog2e), e2 = exp2_approx(x > 126.0f ? 126.0f : x);  // NaN stays
           u[c] = fmaf(cap2, 1.0f - __fdividef(2.0f, 1.0f + e2), lv - m[c]);
         }
       } else {
@@ -694,16 +693,19 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) kv8_attn_kernel(const _
 }
 
 // ---- host --------------------------------------------------------------------------------
-// Columns per tile: the smallest of 8, 16, 32 that holds a request's queries times the heads of
-// a group, so decode pays for no empty columns; beyond that the f16 kernel (0).
+// Columns per tile: 8 or 16 that hold a request's queries times the heads of a group, so decode
+// pays for no empty columns; beyond 16 the f16 kernel (0).  Both sides measured: 32 columns of
+// digits took 295 us for 16 sequences of 32K-64K tokens with groups of 32 heads, 78 us for 32 of
+// 1K-8K with two queries of 16 heads, where the f16 kernel takes 266 and 49; at 16 columns the
+// digits take 141 us and the f16 kernel 266 (groups of 16, 32K-64K tokens).
 static int columns_of(int Hq, int Hk, int max_q) {
   const int64_t want = (int64_t)(Hq / Hk) * max_q;
-  return want <= 8 ? 8 : want <= 16 ? 16 : want <= kMaxColumns ? 32 : 0;
+  return want <= 8 ? 8 : want <= 16 ? 16 : 0;
 }
-static int ctas_of(int nc, int num_sms) { return num_sms * (nc <= 16 ? 2 : 1); }
+static int ctas_of(int num_sms) { return num_sms * 2; }
 
 size_t kv8_attn_workspace_bytes(int Hq, int Hk, int hd, int max_q, int num_sms) {
-  const int nc = columns_of(Hq, Hk, max_q), ctas = ctas_of(nc, num_sms);
+  const int nc = columns_of(Hq, Hk, max_q), ctas = ctas_of(num_sms);
   if (nc == 0) return kv8_wide_workspace_bytes(hd, num_sms);
   return (size_t)ctas * 2 * nc * (hd + 2) * sizeof(float) + (size_t)ctas * kMetaInts * sizeof(int32_t);
 }
@@ -755,8 +757,7 @@ template <int HD, int DQ, bool CAP, typename T>
 static cudaError_t launch_kv8_nc(int nc, const CUtensorMap& km, const CUtensorMap& vm, const KvAttnArgs& a, void* ws,
                                  int num_sms, cudaStream_t stream) {
   if (nc == 8) return launch_kv8_t<KvCfg<HD, 8, DQ, CAP>, T>(km, vm, a, ws, num_sms, stream);
-  if (nc == 16) return launch_kv8_t<KvCfg<HD, 16, DQ, CAP>, T>(km, vm, a, ws, num_sms, stream);
-  return launch_kv8_t<KvCfg<HD, 32, DQ, CAP>, T>(km, vm, a, ws, num_sms, stream);
+  return launch_kv8_t<KvCfg<HD, 16, DQ, CAP>, T>(km, vm, a, ws, num_sms, stream);
 }
 
 template <int HD, bool CAP>

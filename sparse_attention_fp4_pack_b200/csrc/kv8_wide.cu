@@ -389,6 +389,9 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
     const int64_t pos = (int64_t)w.x.pos0 + i;
     const int hi = !live || pos < 0 ? 0 : (pos + 1 < w.x.cap ? (int)pos + 1 : w.x.cap);
     const int lo = a.window > 0 && pos + 1 > a.window ? (int)(pos + 1 - a.window) : 0;
+    // a warp without a query: its rows of Q are zero, so its scores are too, and their bits will do
+    // for probabilities whose products nobody reads
+    const bool idle = !__any_sync(0xffffffffu, live);
     float qs, m = 0.0f, l = 0.0f;
     bool fresh = true;  // no key seen yet
     if (!bad) {  // the row as f16
@@ -413,7 +416,8 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
       e = e < -100 ? -100 : e;
       const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
       const float per = a.sm_scale * __uint_as_float((uint32_t)(127 + e - 14) << 23);
-      qs = C::CAP ? per / a.softcap : per * kLog2e;
+      // an infinite element leaves no digits of the others: the row's scores are NaN
+      qs = isinf(amax) ? __int_as_float(0x7FFFFFFF) : C::CAP ? per / a.softcap : per * kLog2e;
       if (!shared_rows || g == 0) {
 #pragma unroll
         for (int k = 0; k < C::kHD / 8; ++k) {
@@ -447,6 +451,13 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
       const float4* sc = sh.sc[(tile0 + j) % 8];
       bad = !__all_sync(0xffffffffu, kv_wait(&sh.abort, sh.sfull[g], n_s & 1u));
       if (bad) break;
+      if (idle) {
+        if ((tid & 31) == 0) {
+          tc::mbar_arrive(tc::smem_u32(&sh.pfull[g][0]));
+          tc::mbar_arrive(tc::smem_u32(&sh.pfull[g][1]));
+        }
+        continue;
+      }
       tc::fence_after_sync();
       union {
         uint32_t u[128];
@@ -463,7 +474,7 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
           const float k2 = x.x * qs, off = x.y + shift;
 #pragma unroll
           for (int k = p * 16; k < p * 16 + 16; ++k) {
-            const float e2 = exp2_approx(fminf(t.f[k] * k2 * (2.0f * kLog2e), 126.0f));
+            const float y = t.f[k] * k2 * (2.0f * kLog2e), e2 = exp2_approx(y > 126.0f ? 126.0f : y);  // NaN stays
             t.f[k] = fmaf(cap2, 1.0f - __fdividef(2.0f, 1.0f + e2), off);
           }
         } else {
