@@ -1,4 +1,5 @@
-"""Build libcsa2.so (all CUDA sources under csrc/) for sm_100a, in-tree.
+"""Build libcsa2.so (all CUDA sources under csrc/) for sm_100a and _native.so (csrc/binding.cpp, the
+torch-side fast path of the calls made per layer), in-tree.
 
     python -m sparse_attention_fp4_pack_b200.build [--force] [--verbose-ptxas]
 """
@@ -6,12 +7,15 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libcsa2.so")
+BINDING = os.path.join(CSRC, "binding.cpp")
+NATIVE = os.path.join(HERE, "_native.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [
@@ -40,7 +44,31 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in sources() + headers())
 
 
+def build_native(force: bool = False) -> str:
+    """_native.so, linked against libcsa2.so beside it and the installed torch."""
+    deps = [BINDING, os.path.join(INCLUDE, "csa2.h")]
+    if not force and os.path.exists(NATIVE) and all(os.path.getmtime(p) <= os.path.getmtime(NATIVE) for p in deps):
+        return NATIVE
+    from torch.utils import cpp_extension
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    dirs = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(cuda, "include"), *cpp_extension.include_paths()]
+    libs = cpp_extension.library_paths()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           *[f"-isystem{d}" for d in dirs], BINDING, "-o", NATIVE + ".tmp", f"-L{HERE}", "-l:libcsa2.so",
+           "-Wl,-rpath,$ORIGIN", *[f"-L{d}" for d in libs], *[f"-Wl,-rpath,{d}" for d in libs],
+           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    subprocess.run(cmd, check=True)
+    os.replace(NATIVE + ".tmp", NATIVE)
+    return NATIVE
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    build_lib(force, verbose_ptxas)
+    build_native(force)
+    return LIB
+
+
+def build_lib(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     cmd = [NVCC, *FLAGS, "-I", INCLUDE, "-I", CSRC, "-o", LIB + ".tmp", *sources()]

@@ -506,10 +506,26 @@ def csa2_attn_combine(out_parts, lse_parts, out, lse, stream=None):
 
 
 # ---- paged 8-bit KV cache ----------------------------------------------------------------
-# These calls are made per layer of a decode step, where the host's time shows: their checks
-# read each tensor's properties once and explain a refusal only when there is one.
+# These calls are made per layer of a decode step, where the host's time shows: on the current
+# stream they go through _native (csrc/binding.cpp), which makes the same checks in C++.  What it
+# does not take (another stream, an argument that is not as it should be) comes here, where the
+# checks read each tensor's properties once and name what they refuse.
 _BF16, _F16, _I32, _I64, _F32, _U8 = (torch.bfloat16, torch.float16, torch.int32, torch.int64, torch.float32, torch.uint8)
 _KV_DTYPES = {_BF16: 0, _F16: 1}
+
+
+_fast = None
+
+
+def _load_fast():
+    global _fast
+    lib()
+    try:
+        from . import _native
+    except ImportError as e:
+        raise RuntimeError("_native.so is missing; build it with __graft_entry__.build()") from e
+    _fast = _native
+    return _native
 
 
 def _refuse(t, dtype, shape, name, dev):
@@ -595,6 +611,11 @@ def csa2_paged_plan(ctx_len, new_len, block_table, free_pages, n_free, page, n_p
     free_pages i32 [F] with n_free i32 [1] valid -> seq_len i32 [R], n_free_out i32 [1],
     q_start i32 [R+1], slot_map and pos i64 [T_cap] (see include/csa2.h).  seq_len may be
     ctx_len and n_free_out may be n_free."""
+    if stream is None:
+        st = (_fast or _load_fast()).paged_plan(ctx_len, new_len, block_table, free_pages, n_free, page, n_pages, seq_len,
+                                               n_free_out, q_start, slot_map, pos, dev_status)
+        if st >= 0:
+            return _check(st, "csa2_paged_plan")
     dev = ctx_len.get_device()
     R, F, T = _length(ctx_len, "ctx_len"), _length(free_pages, "free_pages"), _length(slot_map, "slot_map")
     ta, cols = _table(block_table, R, dev)
@@ -612,6 +633,11 @@ def csa2_paged_release(seq_len, block_table, release, free_pages, n_free, page, 
     """The pages of requests whose release u8 [R] is nonzero, pushed onto free_pages i32 [F]
     after its n_free i32 [1] entries; seq_len_out i32 [R] (0 for those) and n_free_out i32 [1]
     may be seq_len and n_free."""
+    if stream is None:
+        st = (_fast or _load_fast()).paged_release(seq_len, block_table, release, free_pages, n_free, page, n_pages,
+                                                  seq_len_out, n_free_out, dev_status)
+        if st >= 0:
+            return _check(st, "csa2_paged_release")
     dev = seq_len.get_device()
     R, F = _length(seq_len, "seq_len"), _length(free_pages, "free_pages")
     ta, cols = _table(block_table, R, dev)
@@ -636,6 +662,10 @@ def csa2_kv8_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, dev_stat
     """k, v bf16 or fp16 [T,Hk,hd] (token-strided views allowed) written as E4M3 codes into
     k_cache, v_cache u8 [n_pages,Hk,page,hd] at slot_map i64 [T], with one power-of-two scale
     per page and head in k_scale, v_scale f32 [n_pages,Hk] (see include/csa2.h)."""
+    if stream is None:
+        st = (_fast or _load_fast()).kv8_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, dev_status)
+        if st >= 0:
+            return _check(st, "csa2_kv8_append")
     dev = k.get_device()
     (P, Hk, page, hd), cache = _cache_args(k_cache, v_cache, k_scale, v_scale, dev)
     dtype = k.dtype
@@ -666,6 +696,11 @@ def csa2_kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, q_start, s
     """q bf16 or fp16 [T,Hq,hd] (token-strided views allowed), the cache of csa2_kv8_append,
     block_table i32 [R,max_pages], q_start i32 [R+1], seq_len i32 [R] -> out like q
     (contiguous) and lse f32 [T,Hq] or None (see include/csa2.h)."""
+    if stream is None:
+        st = (_fast or _load_fast()).kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, q_start, seq_len,
+                                             sm_scale, out, lse, max_q, window, softcap, ws, dev_status)
+        if st >= 0:
+            return _check(st, "csa2_kv8_attn")
     dev = q.get_device()
     (P, Hk, page, hd), cache = _cache_args(k_cache, v_cache, k_scale, v_scale, dev)
     dtype, sh = q.dtype, q.shape
