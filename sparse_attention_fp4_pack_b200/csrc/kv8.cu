@@ -210,8 +210,8 @@ cudaError_t launch_paged_plan(const int32_t* ctx_len, const int32_t* new_len, in
 
 // ------------------------------------------------------------------------------------
 // Release.  Every CTA scans the rows' page counts; the pages, laid end to end, are shared out
-// over the cluster's warps, read once to see that all are valid and once (from L1) to be
-// written at their place.  Only when one is not, valid pages are counted row by row instead.
+// over the cluster's warps and read, 32 loads per lane in flight; when all are valid, each is
+// written at its place.  Only when one is not, valid pages are counted row by row instead.
 // ------------------------------------------------------------------------------------
 struct ReleaseArgs {
   const int32_t* seq_len;
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_release_kernel(ReleaseArgs
   __shared__ int32_t s_count[kPlanThreads];
   __shared__ int64_t s_at[kPlanThreads];    // first page of each row, counted from the call's first
   __shared__ int32_t s_rows[kPlanThreads];  // pages of each released row of the chunk, else 0
-  __shared__ uint32_t s_bad[kMaxRanks];
+  __shared__ uint32_t s_bad[2][kMaxRanks];  // by chunk parity: a rank may be a chunk ahead of another's reads
   chain_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned rank = blockIdx.x, ranks = gridDim.x;  // one cluster
@@ -268,45 +268,53 @@ __global__ void __launch_bounds__(kPlanThreads) paged_release_kernel(ReleaseArgs
     s_at[tid] = block_exclusive(rows, s_sums, &total);
     __syncthreads();
     const int live = a.R - r0 < kPlanThreads ? a.R - r0 : kPlanThreads;
-    // a warp takes consecutive pages, eight loads per lane at a time; `use` gets a page's place
+    // a warp takes consecutive pages
     const int64_t each = ((total + (int64_t)ranks * kPlanWarps - 1) / ((int64_t)ranks * kPlanWarps) + 31) & ~(int64_t)31;
     const int64_t p_beg = (int64_t)(rank * kPlanWarps + warp) * each;
     const int64_t p_end = p_beg + each < total ? p_beg + each : total;
-    const auto pages = [&](auto use) {
-      int i = p_beg < p_end ? last_at_most(s_at, live, p_beg) : 0;
-      for (int64_t p = p_beg + lane; p < p_end; p += 8 * 32) {
-        int32_t id[8];
+    // a batch of the warp's pages from p on, kBatch per lane: their loads are all in flight
+    constexpr int kBatch = 32;
+    int32_t id[kBatch];
+    const auto read = [&](int64_t p, int i) {
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const int64_t q = p + x * 32;
-          id[x] = 0;
-          if (q < p_end) {
-            while (i + 1 < live && s_at[i + 1] <= q) ++i;
-            id[x] = a.table[(int64_t)(r0 + i) * a.max_pages + (q - s_at[i])];
-          }
+      for (int x = 0; x < kBatch; ++x) {
+        if (x % 8 == 0 && p + x * 32 >= p_end) break;  // the same for the whole warp
+        const int64_t q = p + x * 32 + lane;
+        if (q < p_end) {
+          while (i + 1 < live && s_at[i + 1] <= q) ++i;
+          id[x] = a.table[(int64_t)(r0 + i) * a.max_pages + (q - s_at[i])];
         }
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          if (p + x * 32 < p_end) use(p + x * 32, id[x]);
       }
     };
     bool all = true;
-    pages([&](int64_t, int32_t id) { all &= id >= 0 && id < a.n_pages; });
+    for (int64_t p = p_beg; p < p_end; p += kBatch * 32) {
+      read(p, last_at_most(s_at, live, p));
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        if (x % 8 == 0 && p + x * 32 >= p_end) break;
+        all &= p + x * 32 + lane >= p_end || (id[x] >= 0 && id[x] < a.n_pages);
+      }
+    }
     uint32_t some = __syncthreads_or(!all);
     if (ranks > 1) {
       if (tid < ranks) {
-        const uint32_t at = tc::mapa(tc::smem_u32(&s_bad[rank]), tid);
+        const uint32_t at = tc::mapa(tc::smem_u32(&s_bad[r0 / kPlanThreads & 1][rank]), tid);
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(some) : "memory");
       }
       cluster_sync_all();  // also: this chunk's inputs are read everywhere
       some = 0;
-      for (unsigned k = 0; k < ranks; ++k) some |= s_bad[k];
+      for (unsigned k = 0; k < ranks; ++k) some |= s_bad[r0 / kPlanThreads & 1][k];
     }
     if (!some) {
-      pages([&](int64_t p, int32_t id) {
-        const int64_t to = n_free + pushed + p;
-        if (to < a.free_cap) a.free_pages[to] = id;
-      });
+      for (int64_t p = p_beg; p < p_end; p += kBatch * 32) {
+        if (p_beg + kBatch * 32 < p_end) read(p, last_at_most(s_at, live, p));  // one batch is still there
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          if (x % 8 == 0 && p + x * 32 >= p_end) break;
+          const int64_t q = p + x * 32 + lane, to = n_free + pushed + q;
+          if (q < p_end && to < a.free_cap) a.free_pages[to] = id[x];
+        }
+      }
     } else {  // the valid pages of each row, counted by one warp for every CTA
       bad |= CSA2_DEV_BAD_INDEX;
       __syncthreads();
