@@ -702,11 +702,13 @@ static int columns_of(int Hq, int Hk, int max_q) {
   const int64_t want = (int64_t)(Hq / Hk) * max_q;
   return want <= 8 ? 8 : want <= 16 ? 16 : 0;
 }
+// Rows per item of the f16 kernel.
+static int rows_of(int Hq, int Hk, int max_q) { return (int64_t)(Hq / Hk) * max_q <= 128 ? 128 : 256; }
 static int ctas_of(int num_sms) { return num_sms * 2; }
 
 size_t kv8_attn_workspace_bytes(int Hq, int Hk, int hd, int max_q, int num_sms) {
   const int nc = columns_of(Hq, Hk, max_q), ctas = ctas_of(num_sms);
-  if (nc == 0) return kv8_wide_workspace_bytes(hd, num_sms);
+  if (nc == 0) return kv8_wide_workspace_bytes(hd, rows_of(Hq, Hk, max_q), num_sms);
   return (size_t)ctas * 2 * nc * (hd + 2) * sizeof(float) + (size_t)ctas * kMetaInts * sizeof(int32_t);
 }
 
@@ -798,7 +800,7 @@ cudaError_t launch_kv8_attn(const void* q, int64_t q_stride, int f16, int64_t T,
   const int nc = columns_of(Hq, Hk, max_q);
   if (!encode_rows(&km, k_cache, rows, hd, page, nc > 0) || !encode_rows(&vm, v_cache, rows, hd, page, nc > 0))
     return cudaErrorInvalidValue;
-  if (nc == 0) return launch_kv8_wide(a, f16, hd, km, vm, ws, num_sms, stream);
+  if (nc == 0) return launch_kv8_wide(a, f16, hd, rows_of(Hq, Hk, max_q), km, vm, ws, num_sms, stream);
   if (hd == 64)
     return softcap > 0.0f ? launch_kv8_type<64, true>(f16, nc, km, vm, a, ws, num_sms, stream)
                           : launch_kv8_type<64, false>(f16, nc, km, vm, a, ws, num_sms, stream);

@@ -453,8 +453,9 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const KvAttnAr
 }
 
 // kv8_wide.cu: the kernel for many rows per key head.
-size_t kv8_wide_workspace_bytes(int hd, int num_sms);
-cudaError_t launch_kv8_wide(const KvAttnArgs& a, int f16, int hd, const CUtensorMap& km, const CUtensorMap& vm, void* ws,
+// rows: 128 or 256, the most of an item.
+size_t kv8_wide_workspace_bytes(int hd, int rows, int num_sms);
+cudaError_t launch_kv8_wide(const KvAttnArgs& a, int f16, int hd, int rows, const CUtensorMap& km, const CUtensorMap& vm, void* ws,
                             int num_sms, cudaStream_t stream);
 
 }  // namespace csa2

@@ -42,16 +42,24 @@ namespace csa2 {
 // 3350 cycles per tile).
 constexpr float kWideLift = 4.0f, kWideSlack = 10.0f;
 
-template <int HD, bool CAP_>
+// ROWS: the most rows of an item, 128 or 256.  With 128 one tile of queries is kept, and the shared
+// memory saved holds more copies in flight, which few rows are bound by: 16 sequences of 32K-64K
+// tokens with groups of 32 heads take 219 us against 260 with the 256-row shape, 8 of 16K-32K with
+// 16 drafts of 8 heads 94 against 109.  Beyond 128 rows a key tile serves 256 at once.
+template <int HD, int ROWS, bool CAP_>
 struct KvWide {
-  static constexpr int kHD = HD, NC = 256;
+  static constexpr int kHD = HD, NC = ROWS;
   static constexpr bool CAP = CAP_;
   static constexpr int kThreads = 512;
   static constexpr uint32_t kHalf = 128 * 128;         // 128 rows of 64 f16, 128-byte swizzle
   static constexpr uint32_t kTile = kHalf * (HD / 64);  // a K, V or Q tile
   static constexpr uint32_t kRaw = kKeys * HD;          // the same tile as E4M3
-  static constexpr int kRing = HD == 128 ? 4 : 6, kStages = HD == 128 ? 2 : 6;
-  static constexpr uint32_t kOffQ = 0, kOffRing = 2 * kTile, kOffRaw = kOffRing + kRing * kTile;
+  static constexpr int kRing = HD == 128 ? 4 : 6, kStages = (HD == 128 ? 2 : 6) + (ROWS == 128 ? (HD == 128 ? 2 : 4) : 0);
+  // per-tile scales kept: a tile's are written before its copy waits for a stage, so the tile whose
+  // place they take must be done when the copies can be kStages + kRing items ahead (two per tile)
+  static constexpr int kScales = HD == 64 ? 16 : 8;
+  static_assert(kStages + kRing <= 2 * kScales - 4, "scales of a tile in use would be overwritten");
+  static constexpr uint32_t kOffQ = 0, kOffRing = (ROWS / 128) * kTile, kOffRaw = kOffRing + kRing * kTile;
   static constexpr uint32_t kSmem = kOffRaw + kStages * kRaw + 1024;
   static constexpr uint32_t kColO = 256;  // S0, S1 (and P in their first 64 columns), O0, O1
   // registers per thread of the softmax, converting and loading / issuing warpgroups; the kernel is
@@ -70,7 +78,7 @@ struct WideShared {
   int take, one_slot;           // the piece the softmax warps are at: its tiles, whether its rows fit a slot
   int rows[C::kStages][2];      // first and last + 1 row of the tile that holds a key of the block
   uint32_t pages[C::kStages];   // bit p: its p-th page exists
-  float4 sc[8][kMaxTilePages];  // per tile and page: k_scale, log2 v_scale, 1 / v_scale
+  float4 sc[C::kScales][kMaxTilePages];  // per tile and page: k_scale, log2 v_scale, 1 / v_scale
 };
 
 template <int N>
@@ -126,7 +134,9 @@ __device__ __forceinline__ void tmem_ld128(uint32_t addr, uint32_t (&r)[128]) {
 }
 
 // Rows of the item that a piece works on; both slots share them when they fit one.
+template <class C>
 __device__ __forceinline__ bool one_slot_rows(const Shape& s, const Walk& w) {
+  if constexpr (C::NC == 128) return true;
   const int i0 = w.qb * s.QB, i1 = i0 + s.QB < w.x.n ? i0 + s.QB : w.x.n;
   return (i1 - i0) * s.HB <= 128;
 }
@@ -178,7 +188,7 @@ __device__ void load_tiles(const KvAttnArgs& a, const Shape& s, WideShared<C>& s
     const auto scales = [&](float2 x) {
       const float vs = fmaxf(x.y, 5.421010862427522e-20f);  // 2^-64
       if (lane < ppt)
-        sh.sc[tile_k % 8][lane] = x.y >= 0.0f ? make_float4(x.x, __log2f(vs), __fdividef(1.0f, vs), 0.0f)
+        sh.sc[tile_k % C::kScales][lane] = x.y >= 0.0f ? make_float4(x.x, __log2f(vs), __fdividef(1.0f, vs), 0.0f)
                                               : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
       ++tile_k;
     };
@@ -309,7 +319,7 @@ __device__ void multiply_wide(WideShared<C>& sh, uint32_t smem, uint32_t tmem) {
     ok = kv_wait_all(sh, sh.qfull[0], piece & 1u) && kv_wait_all(sh, sh.qfull[1], piece & 1u);
     if (!ok) break;
     take = uniform(sh.take);
-    const bool one_slot = uniform(sh.one_slot) != 0;
+    const bool one_slot = C::NC == 128 || uniform(sh.one_slot) != 0;
     ok = tile_there(ring(0, false));
     if (!ok) break;
     tc::fence_after_sync();
@@ -373,14 +383,14 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
   const int tid = threadIdx.x, g = tid >> 7, row = tid & 127;
   const uint32_t lanes = tmem + ((uint32_t)((tid >> 5) & 3) << 21);
   const uint32_t s_at = lanes + g * 128, o_at = lanes + C::kColO + g * C::kHD;
-  float2* joint = reinterpret_cast<float2*>(smem_p + C::kOffQ + C::kTile);  // slot 1's rows are unused then
+  float2* joint = reinterpret_cast<float2*>(smem_p + C::kOffQ);  // every product with the queries is done by then
   const float cap2 = C::CAP ? a.softcap * kLog2e : 0.0f;
   if (tid == 0) a.meta[(int64_t)blockIdx.x * kMetaInts] = 0;
   bool bad = false;
   uint32_t n_s = 0, tile0 = 0, piece = 0;  // this slot's tiles; K tiles and pieces before this piece
   Walk w = {};
   for (w.start(a, s, sh.share); w.left > 0; w.next(a, s), ++piece) {
-    const bool shared_rows = one_slot_rows(s, w);
+    const bool shared_rows = one_slot_rows<C>(s, w);
     const int c = shared_rows ? row : g * 128 + row;
     const int qi = c / s.HB, hd = c - qi * s.HB, i = w.qb * s.QB + qi;
     const int h = w.hh / s.nhb, hb = w.hh % s.nhb;
@@ -448,7 +458,7 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
     const int64_t all_lo = a.window > 0 ? (int64_t)w.x.pos0 + last_q + 1 - a.window : 0;
     const int by = shared_rows ? 2 : 1, first_tile = shared_rows ? g : 0;
     for (int j = first_tile; !bad && j < w.take; j += by, ++n_s) {
-      const float4* sc = sh.sc[(tile0 + j) % 8];
+      const float4* sc = sh.sc[(tile0 + j) % C::kScales];
       bad = !__all_sync(0xffffffffu, kv_wait(&sh.abort, sh.sfull[g], n_s & 1u));
       if (bad) break;
       if (idle) {
@@ -664,8 +674,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) kv8_wide_kernel(const __grid_c
 }
 
 // ---- host ------------------------------------------------------------------------------------
-size_t kv8_wide_workspace_bytes(int hd, int num_sms) {
-  return (size_t)num_sms * 2 * 256 * (hd + 2) * sizeof(float) + (size_t)num_sms * kMetaInts * sizeof(int32_t);
+size_t kv8_wide_workspace_bytes(int hd, int rows, int num_sms) {
+  return (size_t)num_sms * 2 * rows * (hd + 2) * sizeof(float) + (size_t)num_sms * kMetaInts * sizeof(int32_t);
 }
 
 template <class C, typename T>
@@ -687,20 +697,26 @@ static cudaError_t launch_wide_t(KvAttnArgs a, const CUtensorMap& km, const CUte
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int HD, bool CAP>
+template <int HD, int ROWS, bool CAP>
 static cudaError_t launch_wide_type(int f16, const KvAttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, void* ws,
                                     int num_sms, cudaStream_t stream) {
-  return f16 ? launch_wide_t<KvWide<HD, CAP>, __half>(a, km, vm, ws, num_sms, stream)
-             : launch_wide_t<KvWide<HD, CAP>, __nv_bfloat16>(a, km, vm, ws, num_sms, stream);
+  return f16 ? launch_wide_t<KvWide<HD, ROWS, CAP>, __half>(a, km, vm, ws, num_sms, stream)
+             : launch_wide_t<KvWide<HD, ROWS, CAP>, __nv_bfloat16>(a, km, vm, ws, num_sms, stream);
+}
+template <int HD, int ROWS>
+static cudaError_t launch_wide_cap(int f16, const KvAttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, void* ws,
+                                   int num_sms, cudaStream_t stream) {
+  return a.softcap > 0.0f ? launch_wide_type<HD, ROWS, true>(f16, a, km, vm, ws, num_sms, stream)
+                          : launch_wide_type<HD, ROWS, false>(f16, a, km, vm, ws, num_sms, stream);
 }
 
-cudaError_t launch_kv8_wide(const KvAttnArgs& a, int f16, int hd, const CUtensorMap& km, const CUtensorMap& vm, void* ws,
-                            int num_sms, cudaStream_t stream) {
+cudaError_t launch_kv8_wide(const KvAttnArgs& a, int f16, int hd, int rows, const CUtensorMap& km, const CUtensorMap& vm,
+                            void* ws, int num_sms, cudaStream_t stream) {
   if (hd == 64)
-    return a.softcap > 0.0f ? launch_wide_type<64, true>(f16, a, km, vm, ws, num_sms, stream)
-                            : launch_wide_type<64, false>(f16, a, km, vm, ws, num_sms, stream);
-  return a.softcap > 0.0f ? launch_wide_type<128, true>(f16, a, km, vm, ws, num_sms, stream)
-                          : launch_wide_type<128, false>(f16, a, km, vm, ws, num_sms, stream);
+    return rows == 128 ? launch_wide_cap<64, 128>(f16, a, km, vm, ws, num_sms, stream)
+                       : launch_wide_cap<64, 256>(f16, a, km, vm, ws, num_sms, stream);
+  return rows == 128 ? launch_wide_cap<128, 128>(f16, a, km, vm, ws, num_sms, stream)
+                     : launch_wide_cap<128, 256>(f16, a, km, vm, ws, num_sms, stream);
 }
 
 }  // namespace csa2
