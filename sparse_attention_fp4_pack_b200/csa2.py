@@ -4,7 +4,8 @@ Argument marshalling only: every function checks that its tensors' shapes agree 
 sizes it passes (the C entry points take sizes and cannot see a buffer's extent, so a
 smaller buffer would be accessed out of bounds), then their devices, dtypes and layout,
 passes raw device pointers and the current CUDA stream to the C entry point of the same
-name, and raises CSA2Error on a non-OK status.  All compute runs in libcsa2's kernels; there
+name, and raises CSA2Error on a non-OK status (the paged 8-bit cache's calls do the same in
+_native, csrc/binding.cpp).  All compute runs in libcsa2's kernels; there
 is no other code path.  Workspaces are plain uint8 device tensors from torch's
 allocator (``workspace``).
 """
