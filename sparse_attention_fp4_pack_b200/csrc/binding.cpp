@@ -146,7 +146,7 @@ T* read_vector(Args& a, at::ScalarType type, int64_t* n) {
   return static_cast<T*>(t->data_ptr());
 }
 
-PyObject* paged_plan(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+PyObject* paged_plan(PyObject* const* argv, Py_ssize_t argc) {
   Args a{argv, argc};
   int64_t R = 0, F = 0, T = 0;
   int cols = 0;
@@ -171,7 +171,7 @@ PyObject* paged_plan(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   });
 }
 
-PyObject* paged_release(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+PyObject* paged_release(PyObject* const* argv, Py_ssize_t argc) {
   Args a{argv, argc};
   int64_t R = 0, F = 0;
   int cols = 0;
@@ -192,7 +192,7 @@ PyObject* paged_release(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   });
 }
 
-PyObject* kv8_append(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+PyObject* kv8_append(PyObject* const* argv, Py_ssize_t argc) {
   Args a{argv, argc};
   int64_t T = 0, k_stride = 0, v_stride = 0;
   const at::Tensor *k = a.tensor(), *v = a.tensor();
@@ -211,7 +211,7 @@ PyObject* kv8_append(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   });
 }
 
-PyObject* kv8_attn(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+PyObject* kv8_attn(PyObject* const* argv, Py_ssize_t argc) {
   Args a{argv, argc};
   const at::Tensor* q = a.tensor();
   Cache c;
@@ -246,26 +246,33 @@ PyObject* kv8_attn(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   }
   uint32_t* status = a.status();
   if (!a.done() || kind < 0 || R > INT32_MAX || Hq > INT32_MAX) return result(kExplain);
+  return on_device(a.dev, [&](cudaStream_t stream) {
+    if (!ws.defined()) {  // from the current stream's pool, so it is not handed out before the kernels are done
+      const size_t need = csa2_kv8_attn_workspace_size((int)Hq, (int)c.Hk, (int)c.hd, max_q, kind);
+      ws = at::empty({(int64_t)(need > 0 ? need : 1)}, q->options().dtype(at::kByte));
+    }
+    return (long)csa2_kv8_attn(qp, q_stride, kind, T, (int)Hq, (int)c.Hk, (int)c.hd, c.k, c.v, c.ks, c.vs, c.pages,
+                               (int)c.page, table, cols, q_start, seq, (int)R, max_q, scale, window, softcap, out, lse,
+                               ws.data_ptr(), (size_t)ws.numel(), status, stream);
+  });
+}
+
+// What torch throws (a tensor without storage or strides, no memory) is asked again, and
+// reported, by csa2.py.
+template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   try {
-    return on_device(a.dev, [&](cudaStream_t stream) {
-      if (!ws.defined()) {  // from the current stream's pool, so it is not handed out before the kernels are done
-        const size_t need = csa2_kv8_attn_workspace_size((int)Hq, (int)c.Hk, (int)c.hd, max_q, kind);
-        ws = at::empty({(int64_t)(need > 0 ? need : 1)}, q->options().dtype(at::kByte));
-      }
-      return (long)csa2_kv8_attn(qp, q_stride, kind, T, (int)Hq, (int)c.Hk, (int)c.hd, c.k, c.v, c.ks, c.vs, c.pages,
-                                 (int)c.page, table, cols, q_start, seq, (int)R, max_q, scale, window, softcap, out, lse,
-                                 ws.data_ptr(), (size_t)ws.numel(), status, stream);
-    });
-  } catch (const std::exception&) {  // no memory: the Python path asks again and reports it
+    return F(argv, argc);
+  } catch (...) {
     return result(kExplain);
   }
 }
 
 PyMethodDef methods[] = {
-    {"paged_plan", (PyCFunction)(void (*)(void))paged_plan, METH_FASTCALL, nullptr},
-    {"paged_release", (PyCFunction)(void (*)(void))paged_release, METH_FASTCALL, nullptr},
-    {"kv8_append", (PyCFunction)(void (*)(void))kv8_append, METH_FASTCALL, nullptr},
-    {"kv8_attn", (PyCFunction)(void (*)(void))kv8_attn, METH_FASTCALL, nullptr},
+    {"paged_plan", (PyCFunction)(void (*)(void))guarded<paged_plan>, METH_FASTCALL, nullptr},
+    {"paged_release", (PyCFunction)(void (*)(void))guarded<paged_release>, METH_FASTCALL, nullptr},
+    {"kv8_append", (PyCFunction)(void (*)(void))guarded<kv8_append>, METH_FASTCALL, nullptr},
+    {"kv8_attn", (PyCFunction)(void (*)(void))guarded<kv8_attn>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

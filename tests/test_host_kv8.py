@@ -156,6 +156,12 @@ def test_binding_names_the_wrong_argument():
     refused(csa2.csa2_kv8_attn, att, "^out", TypeError, out=att["out"].to(bf))
     refused(csa2.csa2_kv8_attn, att, "^q", q=z(5, 8, 128, dtype=hf))
     refused(csa2.csa2_paged_plan, plan, "^block_table", block_table=z(4, 3).T)
+    # tensors without storage or strides end in an exception too
+    for wrong in (z(3).to_sparse(), z(3, 4).to_sparse(), torch.zeros(3, dtype=torch.int32, device="meta")):
+        with pytest.raises((ValueError, TypeError, RuntimeError)):
+            csa2.csa2_paged_plan(**{**plan, "new_len": wrong})
+    with pytest.raises((ValueError, TypeError, AttributeError)):
+        csa2.csa2_paged_plan(**{**plan, "new_len": [1, 2, 3]})
 
 
 def test_plain_plan_and_release_keep_every_page_once():
