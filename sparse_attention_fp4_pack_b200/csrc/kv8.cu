@@ -8,8 +8,8 @@
 // ctx_len, n_free_out is n_free) is safe because a cluster barrier stands between the last
 // read of a chunk and the first write of it.  Both are bound by latency: a launch, two
 // dependent loads, one or two block-wide scans.  Per call (back to back): plan of 256 requests
-// of one token 4.6 us, of 48 with 24K rows 7.1; release of 8 of 61 requests 6.2, of 256 of 1024
-// with 254K pages 18.2.
+// of one token 4.6 us, of 48 with 24K rows 7.1; release of 8 of 61 requests 4.5, of 256 of 1024
+// with 254K pages 13.5 (20 instructions per page before, 6 now; 18.2).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -56,7 +56,8 @@ __device__ __forceinline__ int64_t block_exclusive(int64_t v, int64_t* warp_sums
 }
 
 // The last i with a[i] <= x, for ascending a[0..n) with a[0] <= x.
-__device__ __forceinline__ int last_at_most(const int64_t* a, int n, int64_t x) {
+template <typename T>
+__device__ __forceinline__ int last_at_most(const T* a, int n, T x) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -236,7 +237,8 @@ constexpr int kMaxRanks = 8;
 __global__ void __launch_bounds__(kPlanThreads) paged_release_kernel(ReleaseArgs a) {
   __shared__ int64_t s_sums[32];
   __shared__ int32_t s_count[kPlanThreads];
-  __shared__ int64_t s_at[kPlanThreads];    // first page of each row, counted from the call's first
+  __shared__ int32_t s_first[kPlanThreads];  // first page of each row, counted from the chunk's first
+  __shared__ int64_t s_at[kPlanThreads];     // place of each row's first valid page in the list
   __shared__ int32_t s_rows[kPlanThreads];  // pages of each released row of the chunk, else 0
   __shared__ uint32_t s_bad[2][kMaxRanks];  // by chunk parity: a rank may be a chunk ahead of another's reads
   chain_enter();
@@ -269,30 +271,43 @@ __global__ void __launch_bounds__(kPlanThreads) paged_release_kernel(ReleaseArgs
     }
     s_rows[tid] = (int32_t)rows;
     int64_t total;
-    s_at[tid] = block_exclusive(rows, s_sums, &total);
+    const int64_t before = block_exclusive(rows, s_sums, &total);
+    s_first[tid] = (int32_t)before;  // used when the chunk's pages count in 32 bits
     __syncthreads();
     const int live = a.R - r0 < kPlanThreads ? a.R - r0 : kPlanThreads;
     // a warp takes consecutive pages
-    const int64_t each = ((total + (int64_t)ranks * kPlanWarps - 1) / ((int64_t)ranks * kPlanWarps) + 31) & ~(int64_t)31;
-    const int64_t p_beg = (int64_t)(rank * kPlanWarps + warp) * each;
-    const int64_t p_end = p_beg + each < total ? p_beg + each : total;
+    const bool fits = total <= INT32_MAX - (1 << 16);
+    const int warps = ranks * kPlanWarps;
+    const int each = fits ? (((int)total + warps - 1) / warps + 31) & ~31 : 0;
+    const int p_beg = (int)(rank * kPlanWarps + warp) * each;
+    const int p_end = !fits ? p_beg : p_beg + each < (int)total ? p_beg + each : (int)total;
     // a batch of the warp's pages from p on, kBatch per lane: their loads are all in flight
     constexpr int kBatch = 32;
     int32_t id[kBatch];
-    const auto read = [&](int64_t p, int i) {
+    const auto read = [&](int p) {
+      int i = last_at_most(s_first, live, p), until;
+      const int32_t* row;  // where position 0 would be if the list were this row's
+      const auto open = [&] {
+        row = a.table + (int64_t)(r0 + i) * a.max_pages - s_first[i];
+        until = i + 1 < live ? s_first[i + 1] : INT32_MAX;
+      };
+      open();
 #pragma unroll
       for (int x = 0; x < kBatch; ++x) {
         if (x % 8 == 0 && p + x * 32 >= p_end) break;  // the same for the whole warp
-        const int64_t q = p + x * 32 + lane;
+        const int q = p + x * 32 + lane;
         if (q < p_end) {
-          while (i + 1 < live && s_at[i + 1] <= q) ++i;
-          id[x] = a.table[(int64_t)(r0 + i) * a.max_pages + (q - s_at[i])];
+          while (q >= until) {
+            ++i;
+            open();
+          }
+          id[x] = row[q];
         }
       }
     };
     bool all = true;
-    for (int64_t p = p_beg; p < p_end; p += kBatch * 32) {
-      read(p, last_at_most(s_at, live, p));
+    for (int p = p_beg; p < p_end; p += kBatch * 32) {
+      read(p);
 #pragma unroll
       for (int x = 0; x < kBatch; ++x) {
         if (x % 8 == 0 && p + x * 32 >= p_end) break;
@@ -309,18 +324,19 @@ __global__ void __launch_bounds__(kPlanThreads) paged_release_kernel(ReleaseArgs
       some = 0;
       for (unsigned k = 0; k < ranks; ++k) some |= s_bad[r0 / kPlanThreads & 1][k];
     }
-    if (!some) {
-      for (int64_t p = p_beg; p < p_end; p += kBatch * 32) {
-        if (p_beg + kBatch * 32 < p_end) read(p, last_at_most(s_at, live, p));  // one batch is still there
+    if (!some && fits) {
+      int32_t* to = a.free_pages + n_free + pushed;
+      const int64_t room = a.free_cap - n_free - pushed;
+      for (int p = p_beg; p < p_end; p += kBatch * 32) {
+        if (p_beg + kBatch * 32 < p_end) read(p);  // one batch is still there
 #pragma unroll
         for (int x = 0; x < kBatch; ++x) {
           if (x % 8 == 0 && p + x * 32 >= p_end) break;
-          const int64_t q = p + x * 32 + lane, to = n_free + pushed + q;
-          if (q < p_end && to < a.free_cap) a.free_pages[to] = id[x];
+          const int q = p + x * 32 + lane;
+          if (q < p_end && q < room) to[q] = id[x];
         }
       }
     } else {  // the valid pages of each row, counted by one warp for every CTA
-      bad |= CSA2_DEV_BAD_INDEX;
       __syncthreads();
       s_count[tid] = 0;
       if (ranks > 1) cluster_sync_all();
@@ -335,6 +351,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_release_kernel(ReleaseArgs
           cnt += id >= 0 && id < a.n_pages;
         }
         cnt = __reduce_add_sync(0xffffffffu, cnt);
+        if (cnt != m) bad |= CSA2_DEV_BAD_INDEX;
         if (lane < ranks) {
           if (ranks > 1) {
             const uint32_t at = tc::mapa(tc::smem_u32(&s_count[i]), lane);
@@ -398,8 +415,9 @@ cudaError_t launch_paged_release(const int32_t* seq_len, const int32_t* table, c
 // encoding: one pass over the input.  Pages are found from the slot map alone: a token leads
 // a unit when the token before it lies in another page.  A unit walks the leaders of `win`
 // consecutive tokens.  Measured: single tokens of 32 sequences and 8 heads 5.0 us per call, 9.5K
-// rows of a fused projection 16.8 us (3.5 TB/s of 58.6 MB; HBM's floor is 8.9).  Finding the
-// leaders by ballot, packed 16-bit maxima and 64 registers (twice the warps) brought 33 -> 17.
+// rows of a fused projection 12.4 us (4.7 TB/s of 58.6 MB; HBM's floor is 8.9).  Finding the
+// leaders by ballot, packed 16-bit maxima and 64 registers (twice the warps) brought 33 -> 17,
+// one branch instead of a select between the two divisions 17 -> 12.
 // ------------------------------------------------------------------------------------
 struct AppendArgs {
   const uint8_t* x[2];  // keys, values (16-bit elements)
@@ -419,12 +437,7 @@ __device__ __forceinline__ float block_scale(float amax) {
   return __uint_as_float((uint32_t)(e < 63 ? 63 : e) << 23);
 }
 
-// 8 values over the scale, encoded.  A power-of-two scale (every scale this call chooses)
-// divides exactly by its reciprocal; a page's earlier scale may be any fp32.
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], float s, float inv, bool pow2) {
-  float y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = pow2 ? x[i] * inv : __fdiv_rn(x[i], s);
+__device__ __forceinline__ uint2 encode8(const float (&y)[8]) {
   return make_uint2(e4m3x2_sat(y[0], y[1]) | (e4m3x2_sat(y[2], y[3]) << 16),
                     e4m3x2_sat(y[4], y[5]) | (e4m3x2_sat(y[6], y[7]) << 16));
 }
@@ -525,7 +538,6 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(AppendArgs a) {
       }
       const float s = fmaxf(block_scale(amax), s_old);
       const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0;
-      const float inv = __fdiv_rn(1.0f, s);
       uint8_t* c0 = cache + (pid * a.Hk + h) * (int64_t)(kPage * HD) + (lane % kLanes) * 8;
       if (off > 0 && s != s_old) {  // earlier rows under the larger scale
         const float ratio = __fdiv_rn(s_old, s);
@@ -540,18 +552,30 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(AppendArgs a) {
             e4m3x4_f32(c.y, x + 4);
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] *= ratio;
-            *p = encode8(x, 1.0f, 1.0f, true);
+            *p = encode8(x);
           }
         }
       }
+      // a power of two (every scale this call chooses) divides exactly by its reciprocal; a page's
+      // earlier scale may be any fp32
+      const auto store = [&](auto over) {
 #pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        const int row = g * 16 + k * kRowsAt + lane / kLanes;
-        if (row >= off && row < off + n) {
-          float x[8];
-          unpack8<T>(raw[k], x);
-          *reinterpret_cast<uint2*>(c0 + row * HD) = encode8(x, s, inv, pow2);
+        for (int k = 0; k < kLoads; ++k) {
+          const int row = g * 16 + k * kRowsAt + lane / kLanes;
+          if (row >= off && row < off + n) {
+            float x[8];
+            unpack8<T>(raw[k], x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = over(x[i]);
+            *reinterpret_cast<uint2*>(c0 + row * HD) = encode8(x);
+          }
         }
+      };
+      if (pow2) {
+        const float inv = __fdiv_rn(1.0f, s);
+        store([&](float x) { return x * inv; });
+      } else {
+        store([&](float x) { return __fdiv_rn(x, s); });
       }
       if (g == 0 && lane == 0) *sp = s;
       if (GW > 1)  // s_amax is free again
