@@ -22,7 +22,7 @@
 // Bound by HBM when the sequences are long (32 of 64K-128K tokens, 4 key heads: 463 us, 6.5 TB/s;
 // 517 in long runs, where the 1000 W cap lowers the clock), by the latency of a tile's softmax
 // (about 1 us) and of an item's start and end (3 us) when they are short or windowed (61 of up to
-// 8191 tokens, window 1024, 8 key heads of 64: 52 us against a floor of 9); one sequence of 4096
+// 8191 tokens, window 1024, 8 key heads of 64: 46 us against a floor of 9); one sequence of 4096
 // takes 15 us, of which the joining of its pieces is 3.
 //
 // Roles: warps 0-3 softmax, then one producer warp (TMA, page ids, scales, queries)
@@ -50,6 +50,12 @@ constexpr float kLift = 6.0f;          // probabilities are 2^(t - max + 6), at 
 __host__ __device__ constexpr int round16(int n) { return (n + 15) / 16 * 16; }
 constexpr uint32_t pow2_cols(int n) { return n <= 32 ? 32u : n <= 64 ? 64u : n <= 128 ? 128u : n <= 256 ? 256u : 512u; }
 
+// CTAs per SM.  A tile of 64 channels is half the bytes for the same softmax, so three are needed
+// to hide it: 143 us against 164 for 16 sequences of 64K-128K tokens, 49 against 56 for 61 windowed
+// ones (four: 141 and 53).  With 128 channels two leave each more copies in flight: 135 against
+// 145 us for 16 of 32K-64K.
+__host__ __device__ constexpr int kv8_ctas(int nc, int hd) { return nc == 8 && hd == 64 ? 3 : 2; }
+
 template <int HD, int NC_, int DQ_, bool CAP_>
 struct KvCfg {
   static constexpr int kHD = HD, NC = NC_, DQ = DQ_;
@@ -61,8 +67,8 @@ struct KvCfg {
   static constexpr uint32_t kQBytes = (NS * HD + 1023) / 1024 * 1024;
   static constexpr uint32_t kPBytes = NP * kKeys;
   static constexpr uint32_t kRawBytes = NC * HD * 2;  // query rows as they come
-  static constexpr int kCtas = 2;  // per SM
-  static constexpr uint32_t kBudget = 112u * 1024u - 4096u;
+  static constexpr int kCtas = kv8_ctas(NC, HD);  // per SM
+  static constexpr uint32_t kBudget = (kCtas == 3 ? 75u : 112u) * 1024u - 4096u;
   static constexpr int kFit = (int)((kBudget - 2 * kQBytes - kPBytes - 2 * kRawBytes) / (2 * kTile));
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static constexpr uint32_t kOffK = 0, kOffV = kStages * kTile, kOffQ = 2 * kStages * kTile, kOffP = kOffQ + 2 * kQBytes;
@@ -710,10 +716,8 @@ static int columns_of(int Hq, int Hk, int max_q) {
 }
 // Rows per item of the f16 kernel.
 static int rows_of(int Hq, int Hk, int max_q) { return (int64_t)(Hq / Hk) * max_q <= 128 ? 128 : 256; }
-static int ctas_of(int num_sms) { return num_sms * 2; }
-
 size_t kv8_attn_workspace_bytes(int Hq, int Hk, int hd, int max_q, int num_sms) {
-  const int nc = columns_of(Hq, Hk, max_q), ctas = ctas_of(num_sms);
+  const int nc = columns_of(Hq, Hk, max_q), ctas = num_sms * kv8_ctas(nc, hd);
   if (nc == 0) return kv8_wide_workspace_bytes(hd, rows_of(Hq, Hk, max_q), num_sms);
   return (size_t)ctas * 2 * nc * (hd + 2) * sizeof(float) + (size_t)ctas * kMetaInts * sizeof(int32_t);
 }
