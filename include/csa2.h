@@ -373,7 +373,8 @@ csa2_status csa2_paged_release(const int32_t* seq_len, const int32_t* block_tabl
  *   k, v  16-bit [T][Hk][hd] (dtype CSA2_BF16 or CSA2_F16); k_stride, v_stride: elements from
  *         one token to the next (0 = Hk*hd; a multiple of 8, so views of a fused projection do)
  *   slot_map int64 [T]: -1 rows are skipped; the rows of one page are consecutive in the batch
- *         and their slots ascend by one (csa2_paged_plan's are so)
+ *         (no -1 and no other page's row between them) and their slots ascend by one
+ *         (csa2_paged_plan's are so)
  * For every page touched and head, K and V apart: the first row written by the call decides
  * what is earlier.  With s_new the smallest power of two >= 2^-64 such that |x| <= 448 s_new
  * for every new x of the page, s = s_new when the call writes the page's row 0, else
@@ -383,8 +384,8 @@ csa2_status csa2_paged_release(const int32_t* seq_len, const int32_t* block_tabl
  * re-scaled any number of times without the rounding adding up.  A NaN is stored as NaN and
  * counts for nothing in s_new; an infinity counts as the largest magnitude (s_new = 2^120) and
  * is stored as 448.  Output is bit-exact with that definition.  Slots outside
- * [-1, n_pages*page) and rows that do not follow their neighbour in the same
- * page are skipped and flag CSA2_DEV_BAD_INDEX. */
+ * [-1, n_pages*page), rows that do not follow their neighbour in the same page, and rows behind
+ * skipped ones inside their page are skipped and flag CSA2_DEV_BAD_INDEX. */
 csa2_status csa2_kv8_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, int dtype, int64_t T,
                             int Hk, int hd, const int64_t* slot_map, uint8_t* k_cache, uint8_t* v_cache,
                             float* k_scale, float* v_scale, int64_t n_pages, int page, uint32_t* dev_status,
@@ -397,14 +398,15 @@ csa2_status csa2_kv8_append(const void* k, const void* v, int64_t k_stride, int6
  *       p = seq_len[r] - n_r + i, which sees tokens max(0, p - window + 1) .. p (window 0: 0 .. p)
  *   max_q  about how many rows a request brings (1 for decode): it picks the tile shape; other
  *       numbers of rows are right too.  It also sizes the workspace.
- *   softcap > 0: scores s become softcap * tanh(s / softcap); 0 leaves them
+ *   softcap in [2^-40, 2^100]: scores s become softcap * tanh(s / softcap); 0 leaves them
  *   out 16-bit [T][Hq][hd];  lse fp32 [T][Hq] (natural log; may be NULL)
  * s = sm_scale * q . (k_scale K), out = softmax(s) (v_scale V).  Both products run on the
  * tcgen05 tensor cores.  Up to 16 rows per key head (max_q * Hq/Hk) they run on the E4M3 codes
  * as stored; the queries enter as E4M3 digits that hold every bf16 / fp16 value to 2^-22 of its
  * row's largest element.  Beyond that the codes enter as f16, which holds them exactly, and the
  * queries as f16 to 2^-38 of that element.  The probabilities are rounded to f16; sums are fp32.
- * Scales: k_scale of magnitude up to 2^100, v_scale in [0, 2^120].
+ * Scales: k_scale of magnitude up to 2^100, v_scale in [0, 2^120] (below 2^-64, which
+ * csa2_kv8_append never goes, it counts as 2^-64).
  * A row that sees no key gives out = 0, lse = -inf.  A NaN or an infinity in a query row gives
  * NaN in that row alone; a NaN key code gives NaN in the rows that see it; a NaN value code may
  * give NaN in any row of its request.  Rows of q outside every request are not read and theirs of

@@ -491,7 +491,9 @@ csa2_status csa2_kv8_attn(const void* q, int64_t q_stride, int dtype, int64_t T,
   if ((st = check_table(R, page, block_table, max_pages, n_pages)) != CSA2_OK) return st;
   if (dtype != CSA2_BF16 && dtype != CSA2_F16) return CSA2_ERR_UNSUPPORTED;
   if (Hq < Hk || Hq % Hk || T < 0 || q_stride < 0 || max_q < 1 || window < 0) return CSA2_ERR_INVALID_ARG;
-  if (!std::isfinite(sm_scale) || !std::isfinite(softcap) || softcap < 0.0f) return CSA2_ERR_INVALID_ARG;
+  if (!std::isfinite(sm_scale)) return CSA2_ERR_INVALID_ARG;
+  // between 2^-40 and 2^100 neither the cap nor a score over it leaves fp32
+  if (!(softcap == 0.0f || (softcap >= 0x1p-40f && softcap <= 0x1p100f))) return CSA2_ERR_INVALID_ARG;
   const int64_t row = (int64_t)Hq * hd;
   q_stride = q_stride ? q_stride : row;
   if (q_stride < row || q_stride % 8) return CSA2_ERR_INVALID_ARG;

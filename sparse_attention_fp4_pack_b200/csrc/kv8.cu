@@ -492,6 +492,17 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(AppendArgs a) {
         if (prev + 1 != slots) bad = CSA2_DEV_BAD_INDEX;
       } else {
         first = true;
+        if ((prev < 0 || prev >= n_slots) && t0 + lane > 0) {  // skipped rows inside a page would give it two units
+          int64_t t = t0 + lane - 2, before = -1;
+          for (int i = 0; i < kPage && t >= 0; ++i, --t) {
+            before = a.slot[t];
+            if (before >= 0 && before < n_slots) break;
+          }
+          if (before >= 0 && before < n_slots && before / kPage == slots / kPage) {
+            bad = CSA2_DEV_BAD_INDEX;
+            first = false;
+          }
+        }
       }
     }
     for (unsigned todo = __ballot_sync(0xffffffffu, first); todo; todo &= todo - 1) {

@@ -161,3 +161,29 @@ def test_binding_refuses_on_the_device():
         csa2.csa2_kv8_attn(s.q, s.kc, s.vc, s.ks, s.vs, s.table, s.q_start, s.seq, 0.1, s.out, max_q=0)
     with pytest.raises(csa2.CSA2Error):
         csa2.csa2_paged_plan(s.ctx, s.new, s.table, s.free, s.n_free, 20, 5, s.seq, s.n_free, s.q_start, s.slot, s.pos)
+
+
+def test_append_skipped_rows_inside_a_page():
+    """A -1 row (or one beyond the pool) between two rows of a page: what follows is refused; -1 rows between pages, at the
+    start and at the end are fine."""
+    gen = torch.Generator().manual_seed(2)
+    x = torch.randn(40, 2, 64, generator=gen).to(BF)
+    slot = [-1, -1] + list(range(16, 22)) + [-1, 999] + list(range(24, 28)) + [-1] * 20 + list(range(48, 52)) + [-1, -1]
+    slot += [-1] * (40 - len(slot))
+    want = list(slot)
+    for i, s in enumerate(slot):
+        if 24 <= s < 28 or s == 999:
+            want[i] = -1
+    kc, vc = (torch.randint(0, 126, (5, 2, 16, 64), generator=gen, dtype=torch.uint8) for _ in range(2))
+    ks, vs = (torch.ones(5, 2) for _ in range(2))
+    got = [t.cuda() for t in (kc, vc, ks, vs)]
+    st = csa2.status_word()
+    csa2.csa2_kv8_append(x.cuda(), x.cuda(), torch.tensor(slot).cuda(), *got, dev_status=st)
+    assert int(st) == csa2.DEV_BAD_INDEX
+    ref.append(x, want, kc, ks)
+    ref.append(x, want, vc, vs)
+    for a, b in zip(got, (kc, vc, ks, vs)):
+        assert torch.equal(a.cpu(), b)
+    st = csa2.status_word()                      # the same without the second run: nothing to flag
+    csa2.csa2_kv8_append(x.cuda(), x.cuda(), torch.tensor(want).cuda(), *got, dev_status=st)
+    assert int(st) == 0

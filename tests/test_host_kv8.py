@@ -95,6 +95,7 @@ def test_attn_refuses(L):
         assert call(f, ATTN, **kw) == UNSUPPORTED, kw
     for kw in (dict(Hq=7), dict(Hq=1), dict(Hk=0), dict(T=-1), dict(R=-1), dict(max_q=0), dict(window=-1), dict(qs=4),
                dict(qs=1020), dict(scale=math.nan), dict(scale=math.inf), dict(cap=-1.0), dict(cap=math.nan),
+               dict(cap=1e-30), dict(cap=3e38), dict(cap=math.inf),
                dict(n_pages=0), dict(ws_bytes=1024), dict(ws=None), dict(ws=P(0x10080))):
         assert call(f, ATTN, **kw) == INVALID, kw
     for name in ("q", "kc", "vc", "ks", "vs", "table", "q_start", "seq", "out"):
