@@ -22,7 +22,7 @@
 // Bound by HBM when the sequences are long (32 of 64K-128K tokens, 4 key heads: 463 us, 6.5 TB/s;
 // 517 in long runs, where the 1000 W cap lowers the clock), by the latency of a tile's softmax
 // (about 1 us) and of an item's start and end (3 us) when they are short or windowed (61 of up to
-// 8191 tokens, window 1024, 8 key heads of 64: 46 us against a floor of 9); one sequence of 4096
+// 8191 tokens, window 1024, 8 key heads of 64: 47 us against a floor of 9); one sequence of 4096
 // takes 15 us, of which the joining of its pieces is 3.
 //
 // Roles: warps 0-3 softmax, then one producer warp (TMA, page ids, scales, queries)
@@ -482,11 +482,18 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
       vs = fmaxf(vs, 5.421010862427522e-20f);  // 2^-64
       const float lv = __log2f(vs), per_v = __fdividef(1.0f, vs);
       if constexpr (C::CAP) {
-        // cap * tanh(x), tanh(x) = 1 - 2 / (1 + e^2x): absolute error near 2^-23 of the cap
+        float most = 0.0f;
 #pragma unroll
         for (int c = 0; c < CW; ++c) {
-          const float x = u[c] * ks * qs[c] * (2.0f * kLog2e), e2 = exp2_approx(x > 126.0f ? 126.0f : x);  // NaN stays
-          u[c] = fmaf(cap2, 1.0f - __fdividef(2.0f, 1.0f + e2), lv - m[c]);
+          u[c] = u[c] * ks * qs[c];
+          most = fmaxf(most, fabsf(u[c]));
+        }
+        if (__all_sync(0xffffffffu, most <= kTanhSmall)) {  // the same for the warp: scores well below the cap
+#pragma unroll
+          for (int c = 0; c < CW; ++c) u[c] = fmaf(cap2, tanh_small(u[c]), lv - m[c]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < CW; ++c) u[c] = fmaf(cap2, tanh_any(u[c]), lv - m[c]);
         }
       } else {
 #pragma unroll

@@ -106,6 +106,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -482,21 +487,48 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
       tmem_ld128(s_at, t.u);
       const int key0 = (w.g.tile + w.off + j) * kKeys;
       const float shift = kWideLift - m;
+      if constexpr (C::CAP) {
+        float most = 0.0f;
 #pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        const float4 x = sc[(p * 16) >> a.page_log2];
-        if constexpr (C::CAP) {
-          // cap * tanh(x), tanh(x) = 1 - 2 / (1 + e^2x): absolute error near 2^-23 of the cap
-          const float k2 = x.x * qs, off = x.y + shift;
+        for (int p = 0; p < 8; ++p) {
+          const float k2 = sc[(p * 16) >> a.page_log2].x * qs;
+          const uint64_t kk = pack2(k2, k2);
 #pragma unroll
-          for (int k = p * 16; k < p * 16 + 16; ++k) {
-            const float y = t.f[k] * k2 * (2.0f * kLog2e), e2 = exp2_approx(y > 126.0f ? 126.0f : y);  // NaN stays
-            t.f[k] = fmaf(cap2, 1.0f - __fdividef(2.0f, 1.0f + e2), off);
+          for (int k = p * 16; k < p * 16 + 16; k += 2) {
+            unpack2(mul2(pack2(t.f[k], t.f[k + 1]), kk), t.f[k], t.f[k + 1]);
+            most = fmaxf(most, fmaxf(fabsf(t.f[k]), fabsf(t.f[k + 1])));
+          }
+        }
+        if (__all_sync(0xffffffffu, most <= kTanhSmall)) {  // the same for the warp: scores well below the cap
+          const uint64_t c1 = pack2(kTanh1, kTanh1), c2 = pack2(kTanh2, kTanh2), c3 = pack2(kTanh3, kTanh3),
+                         c4 = pack2(kTanh4, kTanh4), c5 = pack2(kTanh5, kTanh5), cap = pack2(cap2, cap2);
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            const float o = sc[(p * 16) >> a.page_log2].y + shift;
+            const uint64_t off = pack2(o, o);
+#pragma unroll
+            for (int k = p * 16; k < p * 16 + 16; k += 2) {
+              const uint64_t x = pack2(t.f[k], t.f[k + 1]), z = mul2(x, x);
+              const uint64_t q = fma2(fma2(fma2(fma2(c5, z, c4), z, c3), z, c2), z, c1);
+              unpack2(fma2(cap, fma2(mul2(x, z), q, x), off), t.f[k], t.f[k + 1]);
+            }
           }
         } else {
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            const float off = sc[(p * 16) >> a.page_log2].y + shift;
+#pragma unroll
+            for (int k = p * 16; k < p * 16 + 16; ++k) t.f[k] = fmaf(cap2, tanh_any(t.f[k]), off);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const float4 x = sc[(p * 16) >> a.page_log2];
           const uint64_t k2 = pack2(x.x * qs, x.x * qs), off = pack2(x.y + shift, x.y + shift);
 #pragma unroll
-          for (int k = p * 16; k < p * 16 + 16; k += 2) unpack2(fma2(pack2(t.f[k], t.f[k + 1]), k2, off), t.f[k], t.f[k + 1]);
+          for (int k = p * 16; k < p * 16 + 16; k += 2)
+            unpack2(fma2(pack2(t.f[k], t.f[k + 1]), k2, off), t.f[k], t.f[k + 1]);
         }
       }
       if (key0 + kKeys > all_hi || key0 < all_lo) {
