@@ -23,8 +23,8 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
 __device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  tc::cluster_arrive();
+  tc::cluster_wait();
 }
 
 // Exclusive sum of v over the CTA's threads, and the total.  `warp_sums` holds one value per
@@ -244,6 +244,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_release_kernel(ReleaseArgs
   chain_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned rank = blockIdx.x, ranks = gridDim.x;  // one cluster
+  // a peer's shared memory may be written only when the peer has started: each says so here, and
+  // the wait stands before the first store into a peer, behind the scan and the page loads
+  if (ranks > 1) tc::cluster_arrive();
   const int page = 1 << a.page_log2;
   uint32_t bad = 0;
   int64_t n_free = *a.n_free;
@@ -316,6 +319,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_release_kernel(ReleaseArgs
     }
     uint32_t some = __syncthreads_or(!all);
     if (ranks > 1) {
+      if (r0 == 0) tc::cluster_wait();  // every peer has started (a cluster has requests: it is chosen by their number)
       if (tid < ranks) {
         const uint32_t at = tc::mapa(tc::smem_u32(&s_bad[r0 / kPlanThreads & 1][rank]), tid);
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(some) : "memory");

@@ -360,3 +360,60 @@ def test_attn_strided_queries_other_stream_and_no_lse():
     for _ in range(3):  # the same bits every time
         o, l = run_attn(args, 0.1, max_q=4)
         assert torch.equal(o, base_out) and torch.equal(l, base_lse)
+
+
+# ---- plan and release on the cluster of eight CTAs: more rows and pages than one CTA takes ------
+def test_release_edges_on_a_cluster():
+    """test_release_edges with 2500 requests (three chunks) and a table beyond 16384 entries: bad
+    entries in the first and in the last chunk alone, full lists, cut lengths and bad counts."""
+    rng = np.random.default_rng(18)
+    seq, _, table, left, P = plan_inputs(rng, 2500, 16, 200, 0, 4)
+    assert table.size > 16384
+    free = np.full(P, -5, np.int32)
+    free[:len(left)] = left
+    gone = (rng.integers(0, 3, 2500) > 0).astype(np.uint8)
+    long = np.flatnonzero(seq > 32)  # three pages or more
+    a, b, c, d = long[0], long[long < 1024][-1], long[long >= 2048][0], long[-1]
+    gone[[a, b, c, d]] = 1
+    t2, t3 = table.copy(), table.copy()
+    t2[a, 0], t2[b, 1], t2[c, 0], t2[d, 1] = -1, P + 9, -44, P
+    t3[d, 0] = -7
+    for in_place in (False, True):
+        check_release(seq, table, gone, free, len(left), 16, P, in_place)
+        check_release(seq, t2, gone, free, len(left), 16, P, in_place)   # bad entries in two chunks
+        check_release(seq, t3, gone, free, len(left), 16, P, in_place)   # in the last chunk alone
+    check_release(seq, t2, gone, free[:900].copy(), 7, 16, P, False)     # the list is full in the middle of a chunk
+    check_release(seq, table, gone, free[:900].copy(), 7, 16, P, True)
+    check_release(seq, t2, gone, free[:0].copy(), 0, 16, P, False)       # no list
+    narrow = np.ascontiguousarray(table[:, :7])
+    assert narrow.size > 16384
+    check_release(seq, narrow, gone, free, 0, 16, P, False)              # lengths beyond the table
+    s2 = seq.copy()
+    s2[[7, 1500]] = -3, -70000
+    gone2 = gone.copy()
+    gone2[[7, 1500]] = 1
+    check_release(s2, t2, gone2, free, 2, 16, P, True)                   # negative lengths
+    check_release(seq, table, gone, free, -1, 16, P, False)              # counts that cannot be
+    check_release(seq, table, gone, free, P + 8, 16, P, False)
+    check_release(seq, table, np.zeros(2500, np.uint8), free, 5, 16, P, True)
+
+
+def test_plan_edges_on_a_cluster():
+    """test_plan_edges with 2300 requests (three chunks) and more than 2048 rows."""
+    rng = np.random.default_rng(13)
+    ctx, new, table, free, P = plan_inputs(rng, 2300, 16, 60, 4, 0)
+    T = int(new.sum())
+    assert T > 2048
+    for in_place in (False, True):
+        check_plan(ctx, new, table, free, len(free) // 2, 16, P, T, in_place)      # out of pages in the middle
+        check_plan(ctx, new, table, free, 0, 16, P, T + 3, in_place)               # no page at all
+        check_plan(ctx, new, table, free, len(free) + 3, 16, P, T, in_place)       # count beyond the list
+        check_plan(ctx, new, table, free, -2, 16, P, T, in_place)                  # negative count
+        check_plan(ctx, new, table, free, len(free), 16, P, 2100, in_place)        # rows cut off
+        check_plan(ctx, new, table[:, :3].copy(), free, len(free), 16, P, T, in_place)  # table too narrow
+        check_plan(ctx, new, table, free, len(free), 16, P // 2, T, in_place)      # ids beyond the pool
+        c2, n2 = ctx.copy(), new.copy()
+        c2[[5, 2200]], n2[[9, 1100]] = -7, -1
+        check_plan(c2, n2, table, free, len(free), 16, P, T, in_place)             # negative lengths
+    check_plan(ctx, np.zeros_like(new), table, free, len(free), 16, P, 3000)       # nothing new
+    check_plan(ctx[:0], new[:0], table[:0], free, len(free), 16, P, 3000)          # no requests
