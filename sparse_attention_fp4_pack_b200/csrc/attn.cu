@@ -340,6 +340,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(AttnArgs a) {
   const int T = rank < a.n_tiles ? (a.n_tiles - 1 - rank) / C + 1 : 0;  // tiles rank + k C
   const int r = tid >> 1, hf = tid & 1;              // worker: tile row and half
 
+  // Peers write into this CTA's shared memory at the end: it says here that it has started, and
+  // waits for theirs before its first store into a peer (a CTA without tiles gets there at once).
+  if (C > 1) tc::cluster_arrive();
   // set-up that touches no global memory runs while the predecessor finishes
   if (tid == 0) {
     tc::mbar_init(bar_ka, kWorkers);
@@ -639,7 +642,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(AttnArgs a) {
     // P tile 4 KB of 16: the received partials go to that spare space (rows 16-63 of the dim-
     // blocks, then the P area past the tile, in 6 KB pieces), and the per-head max and sum to
     // the tail of the misc area.  Nothing else reads or writes those bytes, so a CTA may push
-    // as soon as its own products are done: no cluster barrier first.  Otherwise the partials
+    // as soon as its own products are done and its peers have started.  Otherwise the partials
     // go over the key and query tiles, once every CTA of the cluster is done with them.
     const bool spare = NQ == 16 && C * kD * hpc * 4 <= 10 * 6144;
     auto recv_off = [&](uint32_t byte) -> uint32_t {  // shared-memory offset of a received byte
@@ -651,6 +654,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(AttnArgs a) {
     float* rmax = spare ? rml : red_max;
     float* rsum = spare ? rml + C * hpc : red_sum;
     tc::fence_before_sync();
+    tc::cluster_wait();                // every peer has started
     if (!spare) cluster_sync_all();  // every CTA has finished its products: key and query tiles are free
     {
       const int q4 = warp & 3, half = warp >> 2;

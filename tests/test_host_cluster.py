@@ -21,7 +21,7 @@ def kernels(source):
         yield m.group(1), source[m.end():at]
 
 
-@pytest.mark.parametrize("name", ["paged_release_kernel"])
+@pytest.mark.parametrize("name", ["paged_release_kernel", "attn_kernel"])
 def test_a_peer_is_written_after_it_has_started(name):
     found = {}
     for path in build.sources():
