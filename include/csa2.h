@@ -385,7 +385,9 @@ csa2_status csa2_paged_release(const int32_t* seq_len, const int32_t* block_tabl
  * counts for nothing in s_new; an infinity counts as the largest magnitude (s_new = 2^120) and
  * is stored as 448.  Output is bit-exact with that definition.  Slots outside
  * [-1, n_pages*page), rows that do not follow their neighbour in the same page, and rows behind
- * skipped ones inside their page are skipped and flag CSA2_DEV_BAD_INDEX. */
+ * skipped ones inside their page (however many) are skipped and flag CSA2_DEV_BAD_INDEX.  A page
+ * that comes again behind rows of another page is not noticed: what it then holds depends on
+ * timing, the other pages are as defined. */
 csa2_status csa2_kv8_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, int dtype, int64_t T,
                             int Hk, int hd, const int64_t* slot_map, uint8_t* k_cache, uint8_t* v_cache,
                             float* k_scale, float* v_scale, int64_t n_pages, int page, uint32_t* dev_status,

@@ -487,6 +487,7 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(AppendArgs a) {
   for (int64_t t0 = w0; t0 < w1; t0 += 32) {  // the same for every warp of the unit
     int64_t slots = -1;
     bool first = false;  // this lane's token is the first of its page
+    bool behind = false;  // it is, and what is in front of it is skipped
     if (t0 + lane < w1) {
       slots = a.slot[t0 + lane];
       const int64_t prev = t0 + lane > 0 ? a.slot[t0 + lane - 1] : -1;
@@ -496,20 +497,27 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(AppendArgs a) {
         if (prev + 1 != slots) bad = CSA2_DEV_BAD_INDEX;
       } else {
         first = true;
-        if ((prev < 0 || prev >= n_slots) && t0 + lane > 0) {  // skipped rows inside a page would give it two units
-          int64_t t = t0 + lane - 2, before = -1;
-          for (int i = 0; i < kPage && t >= 0; ++i, --t) {
-            before = a.slot[t];
-            if (before >= 0 && before < n_slots) break;
-          }
-          if (before >= 0 && before < n_slots && before / kPage == slots / kPage) {
+        behind = (prev < 0 || prev >= n_slots) && t0 + lane > 0;
+      }
+    }
+    unsigned firsts = __ballot_sync(0xffffffffu, first);
+    // Skipped rows inside a page would give it two units, which would write its scale and rows at the
+    // same time: the nearest row in front that has a slot, however far, must lie in another page.
+    for (unsigned todo = __ballot_sync(0xffffffffu, behind); todo; todo &= todo - 1) {
+      const int from = __ffs(todo) - 1;
+      for (int64_t at = t0 + from - 2; at >= 0; at -= 32) {
+        const int64_t before = at >= lane ? a.slot[at - lane] : -1;
+        const unsigned valid = __ballot_sync(0xffffffffu, before >= 0 && before < n_slots);
+        if (valid) {
+          if (__shfl_sync(0xffffffffu, before, __ffs(valid) - 1) / kPage == __shfl_sync(0xffffffffu, slots, from) / kPage) {
             bad = CSA2_DEV_BAD_INDEX;
-            first = false;
+            firsts &= ~(1u << from);
           }
+          break;
         }
       }
     }
-    for (unsigned todo = __ballot_sync(0xffffffffu, first); todo; todo &= todo - 1) {
+    for (unsigned todo = firsts; todo; todo &= todo - 1) {
       const int from = __ffs(todo) - 1;
       const int64_t t = t0 + from, slot = __shfl_sync(0xffffffffu, slots, from);
       const int64_t pid = slot / kPage;

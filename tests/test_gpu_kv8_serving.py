@@ -187,3 +187,32 @@ def test_append_skipped_rows_inside_a_page():
     st = csa2.status_word()                      # the same without the second run: nothing to flag
     csa2.csa2_kv8_append(x.cuda(), x.cuda(), torch.tensor(want).cuda(), *got, dev_status=st)
     assert int(st) == 0
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_append_long_gaps_inside_a_page(page):
+    """The rows behind a gap inside their page are refused however long the gap is; behind the same
+    gap the rows of another page are written."""
+    gen = torch.Generator().manual_seed(page)
+    for gap in (1, 2, page - 2, page - 1, page, page + 1, page + 2, 3 * page, 1000):
+        run = [3 * page + i for i in range(4)]
+        skipped = [-1] * gap
+        skipped[gap // 2] = 7 * page if gap % 2 else -1          # beyond the pool in some
+        slot = [-1] + run + skipped + [s + 6 for s in run] + [-1] * gap + [s + 10 for s in run] + [page, page + 1]
+        slot += skipped + [5 * page, 5 * page + 1]
+        keep = list(slot)
+        for i, s in enumerate(slot):
+            if s == 7 * page or 3 * page + 6 <= s < 4 * page:
+                keep[i] = -1
+        x, y = (torch.randn(len(slot), 1, 64, generator=gen).to(BF) for _ in range(2))
+        kc, vc = (torch.randint(0, 126, (7, 1, page, 64), generator=gen, dtype=torch.uint8) for _ in range(2))
+        ks, vs = (torch.full((7, 1), 2.0 ** -12) for _ in range(2))
+        got = [t.cuda() for t in (kc, vc, ks, vs)]
+        for again in range(3):
+            st = csa2.status_word()
+            csa2.csa2_kv8_append(x.cuda(), y.cuda(), torch.tensor(slot).cuda(), *got, dev_status=st)
+            assert int(st) == csa2.DEV_BAD_INDEX
+            ref.append(x, keep, kc, ks)
+            ref.append(y, keep, vc, vs)
+            for a, b in zip(got, (kc, vc, ks, vs)):
+                assert torch.equal(a.cpu(), b), gap
