@@ -9,9 +9,10 @@
 //   * a probability (at most 2^8 after its shift) is rounded to f16, which three digits hold
 //     exactly.
 // Digits are extra columns of the same product (N), so they cost no extra reads of the keys.
-// A page's scale multiplies the score of its keys (K) and the probability of its keys (V):
-// exp2(t) with t = score * log2 e + log2(v_scale) is the weight of the key's V codes, and
-// exp2(t) / v_scale its share of the softmax sum, so one running maximum (of t) bounds both.
+// A page's scale multiplies the score of its keys (K) and the probability of its keys (V): with
+// p = exp2(score * log2 e - running maximum), p is the key's share of the softmax sum and
+// p * v_scale the weight of its V codes, in units of the largest v_scale so far (a power of two).
+// The sum is of the scores alone: no value scale, however large, takes a key out of it.
 //
 // S^T[128 keys x N] = K_tile . Q^T, O^T[hd x N] += V_tile^T . P^T.  Keys are the M rows (TMEM
 // lanes), a column is one (query, head of the group); up to NC columns share a tile's keys.
@@ -45,7 +46,7 @@
 
 namespace csa2 {
 
-constexpr float kLift = 6.0f;          // probabilities are 2^(t - max + 6), at most 2^8
+constexpr int kLift = 6;  // weights p v_scale are 2^6 of the largest v_scale's power of two, at most 2^8 (slack 2)
 
 __host__ __device__ constexpr int round16(int n) { return (n + 15) / 16 * 16; }
 constexpr uint32_t pow2_cols(int n) { return n <= 32 ? 32u : n <= 64 ? 64u : n <= 128 ? 128u : n <= 256 ? 256u : 512u; }
@@ -157,6 +158,7 @@ struct KvShared {
     int row;       // of out / lse (token * Hq + head), -1 for padding columns
   } col[2][C::NC];
   float red[4][C::NC];
+  uint32_t top_v[4];  // largest value scale of the warps' keys (bits)
   float linv[C::NC];
 };
 
@@ -451,6 +453,9 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
       l[c] = 0.0f;
     }
     uint32_t unseen = 0xffffffffu >> (32 - CW);  // columns that have seen no key yet
+    // exponent of the least power of two not below the value scales of the piece's keys so far: with
+    // weights p v_scale 2^(kLift - unit_e), O counts in units of 2^(unit_e - kLift)
+    int unit_e = kLeastExp;
     for (int i = 0; i < take; ++i, ++n) {
       const int st = (int)(n % C::kStages);
       bad |= !kv_wait(&sh.abort, sh.sfull[n & 1], (uint32_t)(n >> 1) & 1u);
@@ -479,8 +484,7 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
       const float ks = sh.ks[st][row >> a.page_log2];
       float vs = sh.vs[st][row >> a.page_log2];
       const bool there = vs >= 0.0f && key >= lo && key < hi;
-      vs = fmaxf(vs, 5.421010862427522e-20f);  // 2^-64
-      const float lv = __log2f(vs), per_v = __fdividef(1.0f, vs);
+      vs = fmaxf(vs, kLeastScale);
       if constexpr (C::CAP) {
         float most = 0.0f;
 #pragma unroll
@@ -490,14 +494,14 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
         }
         if (__all_sync(0xffffffffu, most <= kTanhSmall)) {  // the same for the warp: scores well below the cap
 #pragma unroll
-          for (int c = 0; c < CW; ++c) u[c] = fmaf(cap2, tanh_small(u[c]), lv - m[c]);
+          for (int c = 0; c < CW; ++c) u[c] = fmaf(cap2, tanh_small(u[c]), -m[c]);
         } else {
 #pragma unroll
-          for (int c = 0; c < CW; ++c) u[c] = fmaf(cap2, tanh_any(u[c]), lv - m[c]);
+          for (int c = 0; c < CW; ++c) u[c] = fmaf(cap2, tanh_any(u[c]), -m[c]);
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < CW; ++c) u[c] = fmaf(u[c] * ks, qs[c], lv - m[c]);
+        for (int c = 0; c < CW; ++c) u[c] = fmaf(u[c] * ks, qs[c], -m[c]);
       }
       if (!there) {
 #pragma unroll
@@ -507,7 +511,7 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
         for (int c = 0; c < CW; ++c)
           if (key >= sh.col[buf][c].hi || key < sh.col[buf][c].lo) u[c] = -INFINITY;
       }
-      bool exceed = false;
+      bool exceed = there && vs > exp2i(unit_e);
 #pragma unroll
       for (int c = 0; c < CW; ++c) exceed |= u[c] > kSlack;
       if (unseen) {
@@ -524,9 +528,15 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
         for (int c = 0; c < CW; ++c) t[c] = u[c];
         const float top = warp_columns<CW, true>(t, lane);
         if (lane < CW) sh.red[wq][lane] = top;
+        const uint32_t top_v = __reduce_max_sync(0xffffffffu, there ? __float_as_uint(vs) : 0u);
+        if (lane == 0) sh.top_v[wq] = top_v;
         asm volatile("bar.sync 1, 128;" ::: "memory");
         if (i > 0) bad |= !kv_wait(&sh.abort, sh.pvdone, (uint32_t)(n - 1) & 1u);
         tc::fence_after_sync();
+        const uint32_t v01 = max(sh.top_v[0], sh.top_v[1]), v23 = max(sh.top_v[2], sh.top_v[3]);
+        const int grown = max(unit_e, pow2_above_exp(__uint_as_float(max(v01, v23))));
+        const float shrink = grown - unit_e > 126 ? 0.0f : exp2i(unit_e - grown);
+        unit_e = grown;
         float f[CW];
 #pragma unroll
         for (int c = 0; c < CW; ++c) {
@@ -545,7 +555,7 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
             uint32_t o[CW];
             tmem_ld<CW>(lanes + C::kColO + d * C::NC, o);
 #pragma unroll
-            for (int c = 0; c < CW; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f[c]);
+            for (int c = 0; c < CW; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * (f[c] * shrink));
             tmem_st<CW>(lanes + C::kColO + d * C::NC, o);
           }
           tc::tmem_wait_st();
@@ -554,16 +564,17 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
       } else if (i > 0) {
         bad |= !kv_wait(&sh.abort, sh.pvdone, (uint32_t)(n - 1) & 1u);  // P may be written again
       }
+      const float weigh = vs * exp2i(kLift - unit_e);  // at most 2^kLift
       uint32_t dig[3][CW / 4];
 #pragma unroll
       for (int c = 0; c < CW; c += 4) {
         uint32_t b[3][2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float p0 = exp2_approx(u[c + 2 * k] + kLift), p1 = exp2_approx(u[c + 2 * k + 1] + kLift);
-          l[c + 2 * k] = fmaf(p0, per_v, l[c + 2 * k]);
-          l[c + 2 * k + 1] = fmaf(p1, per_v, l[c + 2 * k + 1]);
-          const __half2 ph = __floats2half2_rn(p0, p1);
+          const float p0 = exp2_approx(u[c + 2 * k]), p1 = exp2_approx(u[c + 2 * k + 1]);
+          l[c + 2 * k] += p0;
+          l[c + 2 * k + 1] += p1;
+          const __half2 ph = __floats2half2_rn(p0 * weigh, p1 * weigh);
           uint32_t p = *reinterpret_cast<const uint32_t*>(&ph);
           b[0][k] = e4m3x2_of_f16x2(p);
           p = rest16(p, f16x2_of_e4m3x2(b[0][k]));
@@ -614,9 +625,9 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
 #pragma unroll
       for (int c = 0; c < CW; ++c) mm = row == c ? m[c] : mm;
       const int to = sh.col[buf][row].row;
+      sh.linv[row] = tot != 0.0f ? __fdiv_rn(exp2i(unit_e - kLift), tot) : 0.0f;
       if (whole) {
-        sh.linv[row] = tot != 0.0f ? __fdiv_rn(1.0f, tot) : 0.0f;
-        if (a.lse && to >= 0) a.lse[to] = tot != 0.0f ? (mm + log2f(tot) - kLift) * kLn2 : -INFINITY;
+        if (a.lse && to >= 0) a.lse[to] = tot != 0.0f ? (mm + log2f(tot)) * kLn2 : -INFINITY;
       } else {
         part[C::NC * C::kHD + 2 * (row)] = mm;
         part[C::NC * C::kHD + 2 * (row) + 1] = tot;
@@ -645,7 +656,7 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
           }
         } else {
 #pragma unroll
-          for (int c = 0; c < CW; ++c) part[(c) * C::kHD + row] = o[c];
+          for (int c = 0; c < CW; ++c) part[(c) * C::kHD + row] = o[c] * sh.linv[c];
         }
       }
     }
@@ -768,7 +779,7 @@ static cudaError_t launch_kv8_t(const CUtensorMap& km, const CUtensorMap& vm, Kv
   if (e != cudaSuccess) return e;
   e = launch_chained(kv8_attn_kernel<C, T>, dim3(ctas), dim3(C::kThreads), C::kSmem, stream, 0, km, vm, a);
   if (e != cudaSuccess) return e;
-  e = launch_chained(kv8_merge_kernel<C::NC, C::kHD, T>, dim3(ctas, C::NC / 8), dim3(kMergeThreads), 0, stream, 0, a, kLift);
+  e = launch_chained(kv8_merge_kernel<C::NC, C::kHD, T>, dim3(ctas, C::NC / 8), dim3(kMergeThreads), 0, stream, 0, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

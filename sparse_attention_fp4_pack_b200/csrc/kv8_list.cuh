@@ -42,7 +42,7 @@ struct KvAttnArgs {
   uint32_t* status;
 };
 
-// Partial results of CTA c: slot 0 the piece that continues an item, slot 1 the one that
+// Partial results of CTA c (output over the piece's own sum, maximum, sum): slot 0 the piece that continues an item, slot 1 the one that
 // starts an item and does not end it.  meta: [0] slot 1 is used; then [1] the CTA whose slot 0
 // ends the item, [2] key head * head blocks + head block, [3] query block, [4] first row and
 // [5] number of queries of the request.
@@ -149,6 +149,17 @@ __device__ __forceinline__ float tanh_any(float x) {
   const float small = tanh_small(x), large = tanh_large(x);
   return fabsf(x) <= kTanhSmall ? small : large;
 }
+
+// The least power of two that is not below a positive normal x, and its exponent.
+__device__ __forceinline__ int pow2_above_exp(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return (int)(b >> 23) - 127 + ((b & 0x7FFFFFu) != 0);
+}
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }  // -126 <= e <= 127
+__device__ __forceinline__ float pow2_inverse(float x) { return __uint_as_float(0x7F000000u - __float_as_uint(x)); }
+// What value scales count as at least (csa2_kv8_append goes no lower), and log2 of it.
+constexpr float kLeastScale = 5.421010862427522e-20f;
+constexpr int kLeastExp = -64;
 
 template <typename T>
 __device__ __forceinline__ T from_float(float x);
@@ -414,14 +425,18 @@ __device__ void find_share(const KvAttnArgs& a, const Shape& s, int64_t* sums, S
   __syncthreads();
 }
 
-// Joins the pieces of the item that CTA blockIdx.x starts and does not end: with M the largest
-// of the pieces' maxima, out = sum 2^(m - M) O / sum 2^(m - M) l.  A warp joins one column: its
+// Joins the pieces of the item that CTA blockIdx.x starts and does not end.  A piece left its own
+// output O (divided by its own sum l, so it is of the values' size whatever their scales), its
+// maximum m and l: with M the largest m and w = 2^(m - M) l, out = sum w O / sum w.  A warp joins one column: its
 // lanes first hold the statistics of 32 pieces, then 4 (2 of 64) channels each, so the loads of
 // all pieces are independent.
 constexpr int kMergeThreads = 256;  // 8 columns
+// Sums of weights reach 2^32 (2^30 keys of at most 2^2): 2^-34 keeps the weighted values, up to the
+// largest fp32, in range, and the smallest (2^-73, a scale of 2^-64) normal.
+constexpr float kMergeShift = 34.0f;
 
 template <int NC, int HD, typename T>
-__global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const KvAttnArgs a, float lift) {
+__global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const KvAttnArgs a) {
   constexpr int kPart = NC * (HD + 2), kPer = HD / 32;
   using Vec = std::conditional_t<kPer == 4, float4, float2>;
   chain_enter();
@@ -446,13 +461,14 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const KvAttnAr
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  M += kMergeShift;
   float l = 0.0f, acc[kPer];
 #pragma unroll
   for (int d = 0; d < kPer; ++d) acc[d] = 0.0f;
   for (int k0 = 0; k0 < n; k0 += 32) {
     const float2 v = stats(k0 + lane);
-    const float w = v.y != 0.0f ? exp2f(v.x - M) : 0.0f;
-    l += v.y != 0.0f ? v.y * w : 0.0f;
+    const float w = v.y != 0.0f ? v.y * exp2f(v.x - M) : 0.0f;
+    l += w;
     const int in = n - k0 < 32 ? n - k0 : 32;
 #pragma unroll 8
     for (int k = 0; k < in; ++k) {
@@ -469,7 +485,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const KvAttnAr
   T* out = reinterpret_cast<T*>(a.out) + to * HD + lane * kPer;
 #pragma unroll
   for (int d = 0; d < kPer; ++d) out[d] = from_float<T>(l != 0.0f ? __fdiv_rn(acc[d], l) : 0.0f);
-  if (a.lse && lane == 0) a.lse[to] = l != 0.0f ? (M + log2f(l) - lift) * kLn2 : -INFINITY;
+  if (a.lse && lane == 0) a.lse[to] = l != 0.0f ? (M + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // kv8_wide.cu: the kernel for many rows per key head.

@@ -8,9 +8,12 @@
 // f16 after a power of two has brought its largest element into [2^14, 2^15): exact for bf16 and
 // fp16 down to 2^-28 of that element.  Probabilities are rounded to f16 under a shift of 2^4.
 //   S[128 rows x 128 keys] = Q . K_tile^T,   O[128 rows x hd] += P . V_tile  (P from tensor memory)
-// A page's K scale times the row's scale multiplies the scores of its keys, and log2(v_scale)
-// is added: one fused multiply-add per score.  exp2 of that is the weight of the key's V codes,
-// and over v_scale its share of the softmax sum.
+// A page's K scale times the row's scale multiplies the scores of its keys, and the logarithm of
+// its weight w = v_scale over the largest v_scale of the piece so far (a power of two) is added: one
+// fused multiply-add per score.  exp2 of that is the weight of the key's V codes, and over w its share
+// of the softmax sum.  w counts as 2^kLeastWeight at least (f16 drops what is that small all the same):
+// weights that fp32 cannot hold beside the maximum are then below 2^-60 of the sum as well, so no
+// value scale, however large, takes a key out of it.
 //
 // Two slots of S, P and O keep the tensor cores busy while the other slot's softmax runs:
 //   * more than 128 rows: slot g holds rows 128 g .. of the item, both use every key tile;
@@ -46,7 +49,8 @@ namespace csa2 {
 // they stay below f16's 2^15 and what f16 drops is below 2^-28 of the largest.  The accumulated
 // output is rescaled on a raise; with a slack of 2 one tile in five did (a softmax warp's 561 of
 // 3350 cycles per tile).
-constexpr float kWideLift = 4.0f, kWideSlack = 10.0f;
+constexpr int kWideLift = 4, kLeastWeight = -56;
+constexpr float kWideSlack = 10.0f;
 
 // ROWS: the most rows of an item, 128 or 256.  With 128 one tile of queries is kept, and the shared
 // memory saved holds more copies in flight, which few rows are bound by: 16 sequences of 32K-64K
@@ -84,7 +88,8 @@ struct WideShared {
   int take, one_slot;           // the piece the softmax warps are at: its tiles, whether its rows fit a slot
   int rows[C::kStages][2];      // first and last + 1 row of the tile that holds a key of the block
   uint32_t pages[C::kStages];   // bit p: its p-th page exists
-  float4 sc[C::kScales][kMaxTilePages];  // per tile and page: k_scale, log2 v_scale, 1 / v_scale
+  // per tile and page: k_scale, log2 of w 2^kWideLift, its reciprocal, the unit of w 2^kWideLift
+  float4 sc[C::kScales][kMaxTilePages];
 };
 
 template <int N>
@@ -196,11 +201,14 @@ __device__ void load_tiles(const KvAttnArgs& a, const Shape& s, WideShared<C>& s
         tma_rows(smem + C::kOffRaw + st * C::kRaw + lane * page_bytes, map, (int)(((int64_t)id * a.Hk + h) << a.page_log2), bar);
       ++n;
     };
+    int unit_e = kLeastExp;  // exponent of the largest v_scale of the piece so far
     const auto scales = [&](float2 x) {
-      const float vs = fmaxf(x.y, 5.421010862427522e-20f);  // 2^-64
+      const float vs = fmaxf(x.y, kLeastScale);
+      unit_e = max(unit_e, __reduce_max_sync(0xffffffffu, x.y >= 0.0f ? pow2_above_exp(vs) : kLeastExp));
+      const float w = fmaxf(vs * exp2i(kWideLift - unit_e), exp2i(kLeastWeight)), unit = exp2i(unit_e - kWideLift);
       if (lane < ppt)
-        sh.sc[tile_k % C::kScales][lane] = x.y >= 0.0f ? make_float4(x.x, __log2f(vs), __fdividef(1.0f, vs), 0.0f)
-                                              : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
+        sh.sc[tile_k % C::kScales][lane] = x.y >= 0.0f ? make_float4(x.x, __log2f(w), __fdividef(1.0f, w), unit)
+                                              : make_float4(0.0f, -INFINITY, 0.0f, unit);
       ++tile_k;
     };
     // ids two K tiles ahead, scales one
@@ -394,7 +402,7 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
   const int tid = threadIdx.x, g = tid >> 7, row = tid & 127;
   const uint32_t lanes = tmem + ((uint32_t)((tid >> 5) & 3) << 21);
   const uint32_t s_at = lanes + g * 128, o_at = lanes + C::kColO + g * C::kHD;
-  float2* joint = reinterpret_cast<float2*>(smem_p + C::kOffQ);  // every product with the queries is done by then
+  float4* joint = reinterpret_cast<float4*>(smem_p + C::kOffQ);  // every product with the queries is done by then
   const float cap2 = C::CAP ? a.softcap * kLog2e : 0.0f;
   if (tid == 0) a.meta[(int64_t)blockIdx.x * kMetaInts] = 0;
   bool bad = false;
@@ -413,7 +421,7 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
     // a warp without a query: its rows of Q are zero, so its scores are too, and their bits will do
     // for probabilities whose products nobody reads
     const bool idle = !__any_sync(0xffffffffu, live);
-    float qs, m = 0.0f, l = 0.0f;
+    float qs, m = 0.0f, l = 0.0f, unit = 1.0f;  // unit: what O's numbers count
     bool fresh = true;  // no key seen yet
     if (!bad) {  // the row as f16
       uint4 raw[C::kHD / 8];
@@ -486,7 +494,6 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
       } t;
       tmem_ld128(s_at, t.u);
       const int key0 = (w.g.tile + w.off + j) * kKeys;
-      const float shift = kWideLift - m;
       if constexpr (C::CAP) {
         float most = 0.0f;
 #pragma unroll
@@ -504,7 +511,7 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
                          c4 = pack2(kTanh4, kTanh4), c5 = pack2(kTanh5, kTanh5), cap = pack2(cap2, cap2);
 #pragma unroll
           for (int p = 0; p < 8; ++p) {
-            const float o = sc[(p * 16) >> a.page_log2].y + shift;
+            const float o = sc[(p * 16) >> a.page_log2].y - m;
             const uint64_t off = pack2(o, o);
 #pragma unroll
             for (int k = p * 16; k < p * 16 + 16; k += 2) {
@@ -516,7 +523,7 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
         } else {
 #pragma unroll
           for (int p = 0; p < 8; ++p) {
-            const float off = sc[(p * 16) >> a.page_log2].y + shift;
+            const float off = sc[(p * 16) >> a.page_log2].y - m;
 #pragma unroll
             for (int k = p * 16; k < p * 16 + 16; ++k) t.f[k] = fmaf(cap2, tanh_any(t.f[k]), off);
           }
@@ -525,7 +532,7 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
           const float4 x = sc[(p * 16) >> a.page_log2];
-          const uint64_t k2 = pack2(x.x * qs, x.x * qs), off = pack2(x.y + shift, x.y + shift);
+          const uint64_t k2 = pack2(x.x * qs, x.x * qs), off = pack2(x.y - m, x.y - m);
 #pragma unroll
           for (int k = p * 16; k < p * 16 + 16; k += 2)
             unpack2(fma2(pack2(t.f[k], t.f[k + 1]), k2, off), t.f[k], t.f[k + 1]);
@@ -546,8 +553,10 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
       for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], t.f[124 + x]);
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) - kWideLift;
       const bool raise = fresh ? top > -INFINITY : top > kWideSlack;
-      if (__any_sync(0xffffffffu, raise)) {
-        const float up = raise ? top : 0.0f, f = fresh ? 1.0f : exp2_approx(-up);
+      const float unit_j = sc[0].w;
+      if (__any_sync(0xffffffffu, raise || unit_j != unit)) {
+        const float up = raise ? top : 0.0f, f = fresh ? 1.0f : exp2_approx(-up), f_o = f * (unit * pow2_inverse(unit_j));
+        unit = unit_j;
         m += up;
         l *= f;
         fresh = fresh && !raise;
@@ -559,7 +568,7 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
             uint32_t o[16];
             tc::tmem_ld16(o_at + k, o);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f_o);
             tc::tmem_st16_nowait(o_at + k, o);
           }
         }
@@ -590,16 +599,18 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
     }
     tile0 += w.take;
     if (!bad) bad = !__all_sync(0xffffffffu, kv_wait(&sh.abort, sh.ofull[g], piece & 1u));
-    float f0 = 1.0f, f1 = 0.0f;
-    if (shared_rows) {  // slot 1's maximum and sum to slot 0, which joins them
-      if (g == 1) joint[row] = make_float2(m, l);
+    float f0 = unit, f1 = 0.0f;
+    if (shared_rows) {  // slot 1's maximum, sum and unit to slot 0, which joins them
+      if (g == 1) joint[row] = make_float4(m, l, unit, 0.0f);
       bad = tc::named_sync_or(1, 256, bad);
       if (g == 0) {
-        const float2 o = joint[row];
+        const float4 o = joint[row];
         const float both = l == 0.0f ? o.x : (o.y == 0.0f ? m : fmaxf(m, o.x));
         f0 = l == 0.0f ? 0.0f : exp2f(m - both);
         f1 = o.y == 0.0f ? 0.0f : exp2f(o.x - both);
         l = (l == 0.0f ? 0.0f : l * f0) + (o.y == 0.0f ? 0.0f : o.y * f1);
+        f0 *= unit;
+        f1 *= o.z;
         m = both;
       }
     }
@@ -607,11 +618,11 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
     if (!bad && !(shared_rows && g == 1)) {
       const bool whole = w.first && w.last, join = shared_rows && w.take > 1;
       float* part = a.part + ((int64_t)blockIdx.x * 2 + (w.first ? 1 : 0)) * (C::NC * (C::kHD + 2));
+      const float inv = l != 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+      f0 *= inv;
+      f1 *= inv;
       if (whole) {
-        const float inv = l != 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
-        f0 *= inv;
-        f1 *= inv;
-        if (a.lse && to >= 0) a.lse[to] = l != 0.0f ? (m + log2f(l) - kWideLift) * kLn2 : -INFINITY;
+        if (a.lse && to >= 0) a.lse[to] = l != 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
       } else if (live) {
         *reinterpret_cast<float2*>(part + C::NC * C::kHD + 2 * c) = make_float2(m, l);
       }
@@ -731,7 +742,7 @@ static cudaError_t launch_wide_t(KvAttnArgs a, const CUtensorMap& km, const CUte
   e = launch_chained(kv8_wide_kernel<C, T>, dim3(num_sms), dim3(C::kThreads), C::kSmem, stream, 0, km, vm, a);
   if (e != cudaSuccess) return e;
   e = launch_chained(kv8_merge_kernel<C::NC, C::kHD, T>, dim3(num_sms, C::NC / 8), dim3(kMergeThreads), 0,
-                     stream, 0, a, kWideLift);
+                     stream, 0, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
