@@ -404,9 +404,13 @@ csa2_status csa2_kv8_append(const void* k, const void* v, int64_t k_stride, int6
  *   out 16-bit [T][Hq][hd];  lse fp32 [T][Hq] (natural log; may be NULL)
  * s = sm_scale * q . (k_scale K), out = softmax(s) (v_scale V).  Both products run on the
  * tcgen05 tensor cores.  Up to 16 rows per key head (max_q * Hq/Hk) they run on the E4M3 codes
- * as stored; the queries enter as E4M3 digits that hold every bf16 / fp16 value to 2^-22 of its
- * row's largest element.  Beyond that the codes enter as f16, which holds them exactly, and the
- * queries as f16 to 2^-38 of that element.  The probabilities are rounded to f16; sums are fp32.
+ * as stored; the queries enter as E4M3 digits, which hold elements from 2^-13 of their row's
+ * largest on exactly and smaller ones to 2^-21 of it (bf16; 2^-25 for fp16).  Beyond that the
+ * codes enter as f16, which holds them exactly, and the queries as f16 to 2^-38 of that element.
+ * The sums are fp32 and the softmax sum is of unrounded p = exp(s - max); the weights p * v_scale
+ * of the V codes are rounded to f16: to 2^-11 of themselves, or where they are below 2^-27
+ * (2^-18 beyond 16 rows) of (largest p) * (largest v_scale of the request's pages) to 2^-38 (2^-29)
+ * of that product.
  * Scales: k_scale of magnitude up to 2^100, v_scale in [0, 2^120] (below 2^-64, which
  * csa2_kv8_append never goes, it counts as 2^-64).
  * A row that sees no key gives out = 0, lse = -inf.  A NaN or an infinity in a query row gives

@@ -2,12 +2,15 @@
 //
 // Both products run as tcgen05.mma kind::f8f6f4 with the cache's E4M3 codes as the A operand,
 // exactly as TMA brings them from their pages: nothing is dequantised.  The 16-bit operand of
-// each product is written as a sum of E4M3 digits with weights 1, 1/16, 1/256 instead:
-//   * a query row times a power of two that brings its largest element into [128, 256): two
-//     digits hold every bf16 value (8 significant bits) and three every fp16 value (11)
-//     exactly, down to 2^-22 of the row's largest element;
-//   * a probability (at most 2^8 after its shift) is rounded to f16, which three digits hold
-//     exactly.
+// each product is written as a sum of 8-bit digits instead:
+//   * a query row times a power of two that brings its largest element into [128, 256): E4M3 digits
+//     of weights 1, 1/16 (and 1/256 for fp16).  Elements from 2^-13 of the row's largest on are held
+//     exactly, smaller ones to 2^-21 of it (bf16) or 2^-25 (fp16);
+//   * a weight p * v_scale (at most 2^15 after its shift) is rounded to f16 and held exactly, down to
+//     f16's smallest, by four E5M2 digits of weights 1, 1/8, 1/64, 1/512.  E5M2 has f16's exponents,
+//     so a digit is the upper byte of what is left: three bits of eleven, no conversion.  Three E4M3
+//     digits, as the queries have, would end at 2^-17 of 2^8: a weight e^-12 of the largest was 1% off
+//     and one of e^-17 gone, which shows where the largest meets only zeros in V.
 // Digits are extra columns of the same product (N), so they cost no extra reads of the keys.
 // A page's scale multiplies the score of its keys (K) and the probability of its keys (V): with
 // p = exp2(score * log2 e - running maximum), p is the key's share of the softmax sum and
@@ -46,7 +49,11 @@
 
 namespace csa2 {
 
-constexpr int kLift = 6;  // weights p v_scale are 2^6 of the largest v_scale's power of two, at most 2^8 (slack 2)
+// Weights p v_scale count in 2^-13 of the largest v_scale's power of two: with p at most 2^2 (kSlack) they
+// end at 2^15, below E5M2's 57344, and f16 holds them to half a step down to 2^-27 of that power.
+constexpr int kLift = 13;
+constexpr int kDigitsP = 4;
+constexpr float kDigitP = 0.125f;  // weight of a digit over the one before
 
 __host__ __device__ constexpr int round16(int n) { return (n + 15) / 16 * 16; }
 constexpr uint32_t pow2_cols(int n) { return n <= 32 ? 32u : n <= 64 ? 64u : n <= 128 ? 128u : n <= 256 ? 256u : 512u; }
@@ -62,7 +69,7 @@ struct KvCfg {
   static constexpr int kHD = HD, NC = NC_, DQ = DQ_;
   static constexpr bool CAP = CAP_;
   static constexpr int NS = round16(NC * DQ);   // columns of S
-  static constexpr int NP = round16(NC * 3);    // columns of O
+  static constexpr int NP = round16(NC * kDigitsP);  // columns of O
   static constexpr int kSoft = 128, kThreads = kSoft + 64;
   static constexpr uint32_t kTile = kKeys * HD;  // bytes of a K or V tile
   static constexpr uint32_t kQBytes = (NS * HD + 1023) / 1024 * 1024;
@@ -81,8 +88,9 @@ struct KvCfg {
 };
 
 // ---- primitives ------------------------------------------------------------------------
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
-  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+// A is E4M3, B E4M3 or E5M2.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool a_mn, bool b_mn, bool b_e5m2) {
+  return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
 template <int N>
@@ -120,16 +128,11 @@ __device__ __forceinline__ float warp_columns(float (&v)[N], int lane) {
   return x;
 }
 
-// Two probabilities (f16x2) -> three digits each (two bytes per digit), exactly p = d0 + d1/16
-// + d2/256 while p is a normal f16 of at most 2^8.
-__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-  return r;
-}
-__device__ __forceinline__ uint32_t rest16(uint32_t p, uint32_t d) {  // (p - d) * 16, exact
-  const __half2 r = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&p), *reinterpret_cast<__half2*>(&d)),
-                            __floats2half2_rn(16.0f, 16.0f));
+// What the leading digits of two weights (their upper bytes) leave, times 8, exactly: three bits fewer.
+__device__ __forceinline__ uint32_t next_digit(uint32_t p) {
+  const uint32_t d = p & 0xFF00FF00u;
+  const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&p), *reinterpret_cast<const __half2*>(&d)),
+                            __floats2half2_rn(8.0f, 8.0f));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
@@ -371,8 +374,8 @@ __device__ void produce(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, ui
 // ---- products (one warp) ----------------------------------------------------------------
 template <class C>
 __device__ void multiply(KvShared<C>& sh, uint32_t smem, uint32_t tmem) {
-  constexpr uint32_t kIdS = idesc_e4m3(kKeys, C::NS, false, false);
-  constexpr uint32_t kIdO = idesc_e4m3(128, C::NP, true, true);
+  constexpr uint32_t kIdS = idesc_f8(kKeys, C::NS, false, false, false);
+  constexpr uint32_t kIdO = idesc_f8(128, C::NP, true, true, true);
   // K tile and queries: rows of HD bytes, K-major.  V tile: the same bytes read MN-major (with
   // 64 channels the second half of the 128 M rows repeats the first: leading offset 0).  P:
   // granules of 16 columns x 128 keys, 16 bytes per key, MN-major, no swizzle.
@@ -394,7 +397,7 @@ __device__ void multiply(KvShared<C>& sh, uint32_t smem, uint32_t tmem) {
     const uint32_t d = tmem + C::kColS + (uint32_t)(m & 1) * C::NS;
 #pragma unroll
     for (int k = 0; k < C::kHD / 32; ++k)
-      mma_e4m3(on, d, tc::desc_add(dk, 32 * k), tc::desc_add(dq, 32 * k), kIdS, k > 0);
+      mma_f8(on, d, tc::desc_add(dk, 32 * k), tc::desc_add(dq, 32 * k), kIdS, k > 0);
     commit_if(on, tc::smem_u32(&sh.sfull[m & 1]));
     commit_if(on, tc::smem_u32(&sh.kempty[st]));
   };
@@ -414,7 +417,7 @@ __device__ void multiply(KvShared<C>& sh, uint32_t smem, uint32_t tmem) {
       const uint64_t dv = tc::desc_add(dv0, st * C::kTile);
 #pragma unroll
       for (int k = 0; k < kKeys / 32; ++k)
-        mma_e4m3(on, tmem + C::kColO, tc::desc_add(dv, 32 * k * C::kHD), tc::desc_add(dp, 32 * k * 16), kIdO,
+        mma_f8(on, tmem + C::kColO, tc::desc_add(dv, 32 * k * C::kHD), tc::desc_add(dp, 32 * k * 16), kIdO,
                  i > 0 || k > 0);
       commit_if(on, tc::smem_u32(&sh.vempty[st]));
       commit_if(on, tc::smem_u32(&sh.pvdone));
@@ -547,15 +550,16 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
           f[c] = fresh ? 1.0f : exp2_approx(-up);
           m[c] += up;
           l[c] *= f[c];
+          f[c] *= shrink;  // O counts in the new unit
           u[c] -= up;
         }
         if (i > 0) {  // the accumulated output under the new maxima
 #pragma unroll
-          for (int d = 0; d < 3; ++d) {
+          for (int d = 0; d < kDigitsP; ++d) {
             uint32_t o[CW];
             tmem_ld<CW>(lanes + C::kColO + d * C::NC, o);
 #pragma unroll
-            for (int c = 0; c < CW; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * (f[c] * shrink));
+            for (int c = 0; c < CW; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f[c]);
             tmem_st<CW>(lanes + C::kColO + d * C::NC, o);
           }
           tc::tmem_wait_st();
@@ -565,28 +569,29 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
         bad |= !kv_wait(&sh.abort, sh.pvdone, (uint32_t)(n - 1) & 1u);  // P may be written again
       }
       const float weigh = vs * exp2i(kLift - unit_e);  // at most 2^kLift
-      uint32_t dig[3][CW / 4];
+      uint32_t dig[kDigitsP][CW / 4];
 #pragma unroll
       for (int c = 0; c < CW; c += 4) {
-        uint32_t b[3][2];
+        uint32_t p[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float p0 = exp2_approx(u[c + 2 * k]), p1 = exp2_approx(u[c + 2 * k + 1]);
           l[c + 2 * k] += p0;
           l[c + 2 * k + 1] += p1;
           const __half2 ph = __floats2half2_rn(p0 * weigh, p1 * weigh);
-          uint32_t p = *reinterpret_cast<const uint32_t*>(&ph);
-          b[0][k] = e4m3x2_of_f16x2(p);
-          p = rest16(p, f16x2_of_e4m3x2(b[0][k]));
-          b[1][k] = e4m3x2_of_f16x2(p);
-          p = rest16(p, f16x2_of_e4m3x2(b[1][k]));
-          b[2][k] = e4m3x2_of_f16x2(p);
+          p[k] = *reinterpret_cast<const uint32_t*>(&ph);
         }
 #pragma unroll
-        for (int d = 0; d < 3; ++d) dig[d][c / 4] = b[d][0] | (b[d][1] << 16);
+        for (int d = 0; d < kDigitsP; ++d) {
+          dig[d][c / 4] = __byte_perm(p[0], p[1], 0x7531);
+          if (d + 1 < kDigitsP) {
+            p[0] = next_digit(p[0]);
+            p[1] = next_digit(p[1]);
+          }
+        }
       }
 #pragma unroll
-      for (int d = 0; d < 3; ++d) {
+      for (int d = 0; d < kDigitsP; ++d) {
         const int col = d * C::NC;
         const uint32_t at = smem + C::kOffP + (col / 16) * (16 * kKeys) + row * 16 + col % 16;
         if constexpr (CW == 8) {
@@ -635,17 +640,18 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
     }
     asm volatile("bar.sync 1, 128;" ::: "memory");
     {
-      float o[CW];
-      uint32_t d[CW];
-      tmem_ld<CW>(lanes + C::kColO, d);
+      float o[CW];  // digits of a column are CW columns apart, from the last to the first
 #pragma unroll
-      for (int c = 0; c < CW; ++c) o[c] = __uint_as_float(d[c]);
-      tmem_ld<CW>(lanes + C::kColO + C::NC, d);
+      for (int c = 0; c < CW; ++c) o[c] = 0.0f;
 #pragma unroll
-      for (int c = 0; c < CW; ++c) o[c] = fmaf(__uint_as_float(d[c]), 0.0625f, o[c]);
-      tmem_ld<CW>(lanes + C::kColO + 2 * C::NC, d);
+      for (int x = C::NP - 16; x >= 0; x -= 16) {
+        uint32_t d[16];
+        tc::tmem_ld16(lanes + C::kColO + x, d);
 #pragma unroll
-      for (int c = 0; c < CW; ++c) o[c] = fmaf(__uint_as_float(d[c]), 0.00390625f, o[c]);
+        for (int k = 16 - CW; k >= 0; k -= CW)
+#pragma unroll
+          for (int c = 0; c < CW; ++c) o[c] = fmaf(o[c], kDigitP, __uint_as_float(d[k + c]));
+      }
       if (row < C::kHD) {
         if (whole) {
           T* out = reinterpret_cast<T*>(a.out);

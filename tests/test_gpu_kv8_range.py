@@ -40,3 +40,53 @@ def test_softmax_sum_with_value_scales_far_apart(max_q, news, length, scales):
     want = ref.attn(*args, 0.125, 0, 0.0)
     check_lse(lse, want, f"scales {scales}")
     ref.assert_attn(out, None, want, 0.0, length, f"scales {scales}")
+
+
+def dominated(seed, length, news, nats, hd, dtype):
+    """Requests whose key 0 scores `nats` above the others (give or take one) in every row and has
+    only zeros as its V: the output is carried by the small weights of the other keys."""
+    args = list(attn_inputs(seed, [length, 90], news, 4, 2, hd, 16, dtype))
+    q, kc, vc, ks, vs, table = args[:6]
+    gen = torch.Generator().manual_seed(seed + 1)
+    q[:] = (1.0 + torch.randn(q.shape, generator=gen) / 32).to(dtype)
+    held = kc & 0x7F != 0x7F
+    small = (torch.randn(kc.shape, generator=gen) * 12.0).to(torch.float8_e4m3fn).view(torch.uint8)
+    kc[:] = torch.where(held, small, kc)
+    ks[:], vs[:] = 1.0 / 64, 1.0 / 64
+    code = int(torch.tensor([nats * 64.0 / 8.0]).to(torch.float8_e4m3fn).view(torch.uint8)[0])  # q . k is about hd, sm_scale 8 / hd
+    for r in range(2):
+        kc[table[r, 0].long(), :, 0] = code
+        vc[table[r, 0].long(), :, 0] = 0
+    return args, 8.0 / hd
+
+
+@pytest.mark.parametrize("max_q,news", ROWS[:1])
+@pytest.mark.parametrize("length,hd,dtype", [(200, 64, BF), (2000, 128, BF), (2000, 64, HF)])
+@pytest.mark.parametrize("nats", [8, 12, 16])
+def test_small_weights_beside_a_dominating_key(max_q, news, length, hd, dtype, nats):
+    """Weights down to e^-16 of the largest are held to f16's half step like any other."""
+    args, sm_scale = dominated(31, length, news, nats, hd, dtype)
+    out, lse = run_attn(args, sm_scale, max_q=max_q)
+    want = ref.attn(*args, sm_scale, 0, 0.0)
+    assert (want[0][:1].abs() < 0.1).all()
+    check_lse(lse, want, f"{nats} nats")
+    ref.assert_attn(out, None, want, 0.0, length, f"{nats} nats")
+
+
+@pytest.mark.parametrize("max_q,news", ROWS)
+@pytest.mark.parametrize("spread", [10, 16])
+def test_small_value_scales_beside_a_large_one(max_q, news, spread):
+    """One page holds an outlier in one channel, so its scale is 2^spread times the others'.  The other
+    channels, where it holds zeros, come from the other pages alone and keep f16's half step."""
+    args = list(attn_inputs(33, [600, 90], news, 4, 2, 64, 16, BF, qscale=0.25))
+    vc, vs, table = args[2], args[4], args[5]
+    vs[:] = 2.0 ** -8
+    for r, j in ((0, 11), (1, 0)):
+        page = table[r, j].long()
+        vs[page] = 2.0 ** (spread - 8)
+        vc[page] = 0
+        vc[page, :, 3, 5] = 0x7E  # 448
+    out, lse = run_attn(args, 0.125, max_q=max_q)
+    want = ref.attn(*args, 0.125, 0, 0.0)
+    check_lse(lse, want, f"spread {spread}")
+    ref.assert_attn(out, None, want, 0.0, 600, f"spread {spread}")
