@@ -409,8 +409,8 @@ csa2_status csa2_kv8_append(const void* k, const void* v, int64_t k_stride, int6
  * codes enter as f16, which holds them exactly, and the queries as f16 to 2^-38 of that element.
  * The sums are fp32 and the softmax sum is of unrounded p = exp(s - max); the weights p * v_scale
  * of the V codes are rounded to f16: to 2^-11 of themselves, or where they are below 2^-27
- * (2^-18 beyond 16 rows) of (largest p) * (largest v_scale of the request's pages) to 2^-38 (2^-29)
- * of that product.
+ * (2^-19 beyond 16 rows) of (largest p) * (largest v_scale of the request's pages, up to a power of
+ * two) to 2^-38 (2^-30) of that product.
  * Scales: k_scale of magnitude up to 2^100, v_scale in [0, 2^120] (below 2^-64, which
  * csa2_kv8_append never goes, it counts as 2^-64).
  * A row that sees no key gives out = 0, lse = -inf.  A NaN or an infinity in a query row gives

@@ -6,7 +6,7 @@
 // once: both products are then tcgen05.mma kind::f16 at one column per score, where the digit
 // form of kv8_attn.cu needs two or three.  f16 holds every code exactly.  A query row enters as
 // f16 after a power of two has brought its largest element into [2^14, 2^15): exact for bf16 and
-// fp16 down to 2^-28 of that element.  Probabilities are rounded to f16 under a shift of 2^4.
+// fp16 down to 2^-28 of that element.  Weights are rounded to f16 under a shift of 2^5.
 //   S[128 rows x 128 keys] = Q . K_tile^T,   O[128 rows x hd] += P . V_tile  (P from tensor memory)
 // A page's K scale times the row's scale multiplies the scores of its keys, and the logarithm of
 // its weight w = v_scale over the largest v_scale of the piece so far (a power of two) is added: one
@@ -45,11 +45,12 @@
 
 namespace csa2 {
 
-// Probabilities are 2^(t - m + 4) with m raised only when a score exceeds it by more than 10, so
-// they stay below f16's 2^15 and what f16 drops is below 2^-28 of the largest.  The accumulated
-// output is rescaled on a raise; with a slack of 2 one tile in five did (a softmax warp's 561 of
-// 3350 cycles per tile).
-constexpr int kWideLift = 4, kLeastWeight = -56;
+// Weights are 2^(t - m + 5) with m raised only when a score exceeds it by more than 10, so they end at
+// f16's 2^15; f16 holds them to half a step down to 2^-19 of the largest and drops what is below 2^-30.
+// The accumulated output is rescaled on a raise; with a slack of 2 one tile in five did (a softmax
+// warp's 561 of 3350 cycles per tile).  Six bits more at the low end for a slack of 4 cost 5%: 507
+// against 483 us (drafts), 731 against 687 (chunks).
+constexpr int kWideLift = 5, kLeastWeight = -56;
 constexpr float kWideSlack = 10.0f;
 
 // ROWS: the most rows of an item, 128 or 256.  With 128 one tile of queries is kept, and the shared
