@@ -411,8 +411,9 @@ csa2_status csa2_kv8_append(const void* k, const void* v, int64_t k_stride, int6
  * of the V codes are rounded to f16: to 2^-11 of themselves, or where they are below 2^-27
  * (2^-19 beyond 16 rows) of (largest p) * (largest v_scale of the request's pages, up to a power of
  * two) to 2^-38 (2^-30) of that product.
- * Scales: k_scale of magnitude up to 2^100, v_scale in [0, 2^120] (below 2^-64, which
- * csa2_kv8_append never goes, it counts as 2^-64).
+ * Scales: k_scale of magnitude up to 2^120 (k_scale * sm_scale * q below 2^127 for every element
+ * of q), v_scale in [0, 2^120] (below 2^-64, which csa2_kv8_append never goes, it counts as 2^-64).
+ * A score past fp32's range counts as an infinity: +inf gives NaN in its row, -inf no weight.
  * A row that sees no key gives out = 0, lse = -inf.  A NaN or an infinity in a query row gives
  * NaN in that row alone; a NaN key code gives NaN in the rows that see it; a NaN value code may
  * give NaN in any row of its request.  Rows of q outside every request are not read and theirs of

@@ -257,7 +257,7 @@ __device__ __forceinline__ bool prepare_queries(const KvAttnArgs& a, const Shape
   for (int k = 0; k < kCols; ++k) {
     const int c = k * 4 + warp;
     int e = (int)(__float_as_uint(amax[k]) >> 23) - 127;  // amax in [2^e, 2^(e+1))
-    e = e < -100 ? -100 : e;
+    e = e < -118 ? -118 : e;  // both powers of two below are normal
     const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) x[k][i] *= up;
@@ -492,7 +492,7 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
         float most = 0.0f;
 #pragma unroll
         for (int c = 0; c < CW; ++c) {
-          u[c] = u[c] * ks * qs[c];
+          u[c] *= ks * qs[c];
           most = fmaxf(most, fabsf(u[c]));
         }
         if (__all_sync(0xffffffffu, most <= kTanhSmall)) {  // the same for the warp: scores well below the cap
@@ -504,7 +504,7 @@ __device__ void soften(const KvAttnArgs& a, const Shape& s, KvShared<C>& sh, uin
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < CW; ++c) u[c] = fmaf(u[c] * ks, qs[c], -m[c]);
+        for (int c = 0; c < CW; ++c) u[c] = fmaf(u[c], ks * qs[c], -m[c]);  // the scales first: u * ks may leave fp32
       }
       if (!there) {
 #pragma unroll

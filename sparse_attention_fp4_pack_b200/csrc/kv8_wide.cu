@@ -443,7 +443,7 @@ __device__ void soften_wide(const KvAttnArgs& a, const Shape& s, WideShared<C>& 
         for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
       }
       int e = (int)(__float_as_uint(amax) >> 23) - 127;  // amax in [2^e, 2^(e+1))
-      e = e < -100 ? -100 : e;
+      e = e < -112 ? -112 : e;  // both powers of two below are normal
       const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
       const float per = a.sm_scale * __uint_as_float((uint32_t)(127 + e - 14) << 23);
       // an infinite element leaves no digits of the others: the row's scores are NaN

@@ -98,3 +98,60 @@ def test_small_value_scales_beside_a_large_one(max_q, news, spread):
     want = ref.attn(*args, 0.125, 0, 0.0)
     check_lse(lse, want, f"spread {spread}")
     ref.assert_attn(out, None, want, 0.0, 600, f"spread {spread}")
+
+
+@pytest.mark.parametrize("max_q,news", ROWS)
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("exponent", [100, 120])
+def test_large_key_scales(max_q, news, cap, exponent):
+    """Key scales up to the largest that csa2_kv8_append chooses: scores that fp32 holds are right
+    whatever the scale and the query they come from."""
+    args = list(attn_inputs(41, [700, 90], news, 4, 2, 64, 16, BF))
+    args[0] = (args[0].float() * 2.0 ** (3 - exponent)).to(BF)
+    args[3][:] = args[3] * 2.0 ** exponent
+    out, lse = run_attn(args, 0.125, cap=cap, max_q=max_q)
+    want = ref.attn(*args, 0.125, 0, cap)
+    ref.assert_attn(out, lse, want, cap, 700, f"2^{exponent}")
+
+
+@pytest.mark.parametrize("max_q,news", ROWS)
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_an_infinite_key_is_appended_and_read(max_q, news, cap):
+    """csa2_kv8_append stores an infinity as 448 under a scale of 2^120.  Rows that see that key give it
+    all their weight or none, or are NaN where its score leaves fp32; other rows and heads are as ever."""
+    n, Hk, hd, page, at = news[0], 2, 64, 16, 333
+    args = list(attn_inputs(43, [350, 90], news, 4, Hk, hd, page, BF))
+    gen = torch.Generator().manual_seed(5)
+    x, y = (torch.randn(350, Hk, hd, generator=gen).to(BF) for _ in range(2))
+    x[at, 1, 7] = math.inf
+    slot = [int(args[5][0, p // page]) * page + p % page for p in range(350)]
+    cache = [t.cuda() for t in args[1:5]]
+    csa2.csa2_kv8_append(x.cuda(), y.cuda(), torch.tensor(slot).cuda(), *cache)
+    args[1:5] = [t.cpu() for t in cache]
+    assert (args[3] == 2.0 ** 120).sum() == 1
+    args[0][:, :, 7] = torch.where(torch.rand(args[0].shape[:2], generator=gen) < 0.5, 1.5, -1.5).to(BF)
+    out, lse = run_attn(args, 0.125, cap=cap, max_q=max_q)
+    exact, exact_lse, absum, smax = ref.attn(*args, 0.125, 0, cap)
+    rows = ~torch.isnan(exact_lse[:, 0])
+    small = torch.where(smax < 2.0 ** 60, smax, torch.full_like(smax, cap + 4.0))  # of the scores that share the weight
+    ref.assert_attn(out, None, (exact, exact_lse, absum, small), cap, 350, "an infinite key")
+    err = (lse.cpu().double() - exact_lse).abs()[rows]
+    assert (err <= 2.0 ** -16 * (exact_lse.abs()[rows] + small[rows] + cap + 1.0)).all()
+    big = list(args)
+    big[0] = args[0].clone()
+    big[0][:n] = args[0][:n] * 2.0 ** 7                   # the infinite key's scores leave fp32
+    out, lse = run_attn(big, 0.125, cap=cap, max_q=max_q)
+    exact, exact_lse, absum, smax = ref.attn(*big, 0.125, 0, cap)
+    if not cap:
+        sees = torch.zeros(out.shape[:2], dtype=torch.bool)
+        sees[:n, 2:] = (350 - n + torch.arange(n) >= at)[:, None] & (big[0][:n, 2:, 7] > 0)
+        assert sees.any() and torch.isnan(out.cpu()[sees]).all() and torch.isnan(lse.cpu()[sees]).all()
+        exact_lse[sees] = math.nan
+        finite = ~torch.isnan(exact_lse)
+        assert not torch.isnan(out.cpu()[finite]).any() and not torch.isnan(lse.cpu()[finite]).any()
+        exact, absum = (torch.where(finite[..., None], t, torch.zeros_like(t)) for t in (exact, absum))
+        out = torch.where(finite[..., None], out.cpu(), torch.zeros_like(out.cpu()))
+        exact_lse[~finite] = 0.0
+        exact_lse[n + news[1]:] = math.nan
+    small = torch.where(smax < 2.0 ** 60, smax, torch.full_like(smax, 2.0 ** 10))
+    ref.assert_attn(out, None, (exact, exact_lse, absum, small), cap, 350, "scores past fp32")
