@@ -11,6 +11,7 @@ allocator (``workspace``).
 """
 import ctypes
 import functools
+import operator
 import os
 
 import torch
@@ -571,6 +572,14 @@ def _flag_arg(dev_status, dev):
     return dev_status.data_ptr()
 
 
+def _whole(x, name, bits=32):
+    """x as an int that `bits` bits hold: ctypes would cut a larger one without a word."""
+    v = operator.index(x)
+    if not -(1 << (bits - 1)) <= v < 1 << (bits - 1):
+        raise ValueError(f"{name} must fit a signed {bits}-bit integer, got {v}")
+    return v
+
+
 def _need_cuda(dev, name):
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -617,6 +626,7 @@ def csa2_paged_plan(ctx_len, new_len, block_table, free_pages, n_free, page, n_p
                                                n_free_out, q_start, slot_map, pos, dev_status)
         if st >= 0:
             return _check(st, "csa2_paged_plan")
+    page, n_pages = _whole(page, "page"), _whole(n_pages, "n_pages", 64)
     dev = ctx_len.get_device()
     R, F, T = _length(ctx_len, "ctx_len"), _length(free_pages, "free_pages"), _length(slot_map, "slot_map")
     ta, cols = _table(block_table, R, dev)
@@ -639,6 +649,7 @@ def csa2_paged_release(seq_len, block_table, release, free_pages, n_free, page, 
                                                   seq_len_out, n_free_out, dev_status)
         if st >= 0:
             return _check(st, "csa2_paged_release")
+    page, n_pages = _whole(page, "page"), _whole(n_pages, "n_pages", 64)
     dev = seq_len.get_device()
     R, F = _length(seq_len, "seq_len"), _length(free_pages, "free_pages")
     ta, cols = _table(block_table, R, dev)
@@ -689,6 +700,7 @@ def _kv8_ws(dev, Hq, Hk, hd, max_q, kind):
 
 
 def csa2_kv8_attn_workspace_size(Hq, Hk, hd, max_q, dtype=torch.bfloat16):
+    Hq, Hk, hd, max_q = _whole(Hq, "Hq"), _whole(Hk, "Hk"), _whole(hd, "hd"), _whole(max_q, "max_q")
     return lib().csa2_kv8_attn_workspace_size(Hq, Hk, hd, max_q, _KV_DTYPES[dtype])
 
 
@@ -702,6 +714,7 @@ def csa2_kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, q_start, s
                                              sm_scale, out, lse, max_q, window, softcap, ws, dev_status)
         if st >= 0:
             return _check(st, "csa2_kv8_attn")
+    max_q, window = _whole(max_q, "max_q"), _whole(window, "window")
     dev = q.get_device()
     (P, Hk, page, hd), cache = _cache_args(k_cache, v_cache, k_scale, v_scale, dev)
     dtype, sh = q.dtype, q.shape

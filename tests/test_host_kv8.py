@@ -199,3 +199,27 @@ def test_plain_append_error_is_half_a_step():
     want = x.to(torch.float64)
     slack = 4 * 2.0 ** -10 * scale[1].to(torch.float64)[None, :, None]
     assert ((got - want).abs() <= want.abs() * 2.0 ** -4 + slack).all()
+
+
+def test_binding_refuses_integers_that_do_not_fit():
+    """A window, page or count past the C type's range is refused, not cut to its lower bits."""
+    i64, u8, f32, bf = torch.int64, torch.uint8, torch.float32, torch.bfloat16
+    plan = dict(ctx_len=z(3), new_len=z(3), block_table=z(3, 4), free_pages=z(9), n_free=z(1), page=16, n_pages=20,
+                seq_len=z(3), n_free_out=z(1), q_start=z(4), slot_map=z(7, dtype=i64), pos=z(7, dtype=i64))
+    rel = dict(seq_len=z(3), block_table=z(3, 4), release=z(3, dtype=u8), free_pages=z(9), n_free=z(1), page=16,
+               n_pages=20, seq_len_out=z(3), n_free_out=z(1))
+    cache = dict(k_cache=z(20, 2, 16, 64, dtype=u8), v_cache=z(20, 2, 16, 64, dtype=u8), k_scale=z(20, 2, dtype=f32),
+                 v_scale=z(20, 2, dtype=f32))
+    att = dict(q=z(5, 8, 64, dtype=bf), **cache, block_table=z(3, 4), q_start=z(4), seq_len=z(3), sm_scale=0.1,
+               out=z(5, 8, 64, dtype=bf), lse=z(5, 8, dtype=f32))
+    for fn, base in ((csa2.csa2_paged_plan, plan), (csa2.csa2_paged_release, rel)):
+        refused(fn, base, "^page", page=(1 << 32) + 16)
+        refused(fn, base, "^n_pages", n_pages=(1 << 64) + 20)
+        refused(fn, base, "CUDA", page=np.int64(16))
+        refused(fn, base, "", TypeError, page=16.0)
+    for wide in ((1 << 32) + 5, 1 << 31, -(1 << 33)):
+        refused(csa2.csa2_kv8_attn, att, "^window", window=wide)
+        refused(csa2.csa2_kv8_attn, att, "^max_q", max_q=wide)
+        with pytest.raises(ValueError, match="^max_q"):
+            csa2.csa2_kv8_attn_workspace_size(8, 2, 64, wide)
+    refused(csa2.csa2_kv8_attn, att, "", TypeError, window=1.5)
