@@ -4,6 +4,7 @@ torch-side fast path of the calls made per layer), in-tree.
     python -m sparse_attention_fp4_pack_b200.build [--force] [--verbose-ptxas]
 """
 import glob
+import importlib.metadata
 import os
 import subprocess
 import sys
@@ -16,6 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libcsa2.so")
 BINDING = os.path.join(CSRC, "binding.cpp")
 NATIVE = os.path.join(HERE, "_native.so")
+NATIVE_FOR = os.path.join(HERE, "_native.built_for")  # the Python and torch that _native.so was built for
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [
@@ -44,10 +46,23 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in sources() + headers())
 
 
+def native_for() -> str:
+    """What _native.so's binary interface depends on besides its sources."""
+    return f"python {sys.version} in {sys.prefix}, torch {importlib.metadata.version('torch')}"
+
+
+def native_up_to_date() -> bool:
+    if not os.path.exists(NATIVE) or not os.path.exists(NATIVE_FOR):
+        return False
+    with open(NATIVE_FOR) as f:
+        if f.read() != native_for():
+            return False
+    return all(os.path.getmtime(p) <= os.path.getmtime(NATIVE) for p in (BINDING, os.path.join(INCLUDE, "csa2.h")))
+
+
 def build_native(force: bool = False) -> str:
     """_native.so, linked against libcsa2.so beside it and the installed torch."""
-    deps = [BINDING, os.path.join(INCLUDE, "csa2.h")]
-    if not force and os.path.exists(NATIVE) and all(os.path.getmtime(p) <= os.path.getmtime(NATIVE) for p in deps):
+    if not force and native_up_to_date():
         return NATIVE
     from torch.utils import cpp_extension
     cuda = os.path.dirname(os.path.dirname(NVCC))
@@ -59,6 +74,8 @@ def build_native(force: bool = False) -> str:
            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     subprocess.run(cmd, check=True)
     os.replace(NATIVE + ".tmp", NATIVE)
+    with open(NATIVE_FOR, "w") as f:
+        f.write(native_for())
     return NATIVE
 
 

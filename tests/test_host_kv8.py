@@ -223,3 +223,15 @@ def test_binding_refuses_integers_that_do_not_fit():
         with pytest.raises(ValueError, match="^max_q"):
             csa2.csa2_kv8_attn_workspace_size(8, 2, 64, wide)
     refused(csa2.csa2_kv8_attn, att, "", TypeError, window=1.5)
+
+
+def test_binding_is_rebuilt_for_another_torch_or_python(L, monkeypatch, tmp_path):
+    """_native.so goes by the torch and Python it was built for, not by file times alone."""
+    libbuild.build_native()
+    assert libbuild.native_up_to_date()
+    monkeypatch.setattr(libbuild.importlib.metadata, "version", lambda name: "0.0.1")
+    assert not libbuild.native_up_to_date()
+    monkeypatch.undo()
+    assert libbuild.native_up_to_date()
+    monkeypatch.setattr(libbuild, "NATIVE_FOR", str(tmp_path / "none"))
+    assert not libbuild.native_up_to_date()
