@@ -8,8 +8,8 @@
 // ctx_len, n_free_out is n_free) is safe because a cluster barrier stands between the last
 // read of a chunk and the first write of it.  Both are bound by latency: a launch, two
 // dependent loads, one or two block-wide scans.  Per call (back to back): plan of 256 requests
-// of one token 4.6 us, of 48 with 24K rows 7.1; release of 8 of 61 requests 4.5, of 256 of 1024
-// with 254K pages 13.5 (20 instructions per page before, 6 now; 18.2).
+// of one token 4.6 us, of 48 with 24K rows 7.1; release of 8 of 61 requests 4.7, of 256 of 1024
+// with 254K pages 13.8 (20 instructions per page before, 6 now; 18.2).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -418,8 +418,8 @@ cudaError_t launch_paged_release(const int32_t* seq_len, const int32_t* table, c
 // whole 128 to 256 byte rows and all of them are in registers between the amax and the
 // encoding: one pass over the input.  Pages are found from the slot map alone: a token leads
 // a unit when the token before it lies in another page.  A unit walks the leaders of `win`
-// consecutive tokens.  Measured: single tokens of 32 sequences and 8 heads 5.0 us per call, 9.5K
-// rows of a fused projection 12.4 us (4.7 TB/s of 58.6 MB; HBM's floor is 8.9).  Finding the
+// consecutive tokens.  Measured: single tokens of 32 sequences and 8 heads 4.9 us per call, 9.5K
+// rows of a fused projection 12.75 us (4.6 TB/s of 58.6 MB; HBM's floor is 8.9).  Finding the
 // leaders by ballot, packed 16-bit maxima and 64 registers (twice the warps) brought 33 -> 17,
 // one branch instead of a select between the two divisions 17 -> 12.
 // ------------------------------------------------------------------------------------

@@ -23,11 +23,11 @@
 // the tiles each block sees.  CTA c takes the c-th of equal shares of it; an item cut by a
 // share's border leaves partial sums in the workspace and kv8_merge_kernel joins them.
 //
-// Bound by HBM when the sequences are long (32 of 64K-128K tokens, 4 key heads: 463 us, 6.5 TB/s;
-// 517 in long runs, where the 1000 W cap lowers the clock), by the latency of a tile's softmax
-// (about 1 us) and of an item's start and end (3 us) when they are short or windowed (61 of up to
-// 8191 tokens, window 1024, 8 key heads of 64: 47 us against a floor of 9); one sequence of 4096
-// takes 15 us, of which the joining of its pieces is 3.
+// Bound by HBM when the sequences are long (32 of 64K-128K tokens, 4 key heads: 476 us, 6.3 TB/s;
+// 520 where the 1000 W cap lowers the clock; 16 of 32K-64K 132 us in bf16 and in fp16), by the latency
+// of a tile's softmax (about 1 us) and of an item's start and end (3 us) when they are short or
+// windowed (61 of up to 8191 tokens, window 1024, 8 key heads of 64: 50 us against a floor of 9); one
+// sequence of 4096 takes 15.4 us, of which the joining of its pieces is 3.
 //
 // Roles: warps 0-3 softmax, then one producer warp (TMA, page ids, scales, queries)
 // and one warp that issues the products.  The producer works ahead: a piece's tiles, query rows
@@ -730,10 +730,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) kv8_attn_kernel(const _
 
 // ---- host --------------------------------------------------------------------------------
 // Columns per tile: 8 or 16 that hold a request's queries times the heads of a group, so decode
-// pays for no empty columns; beyond 16 the f16 kernel (0).  Both sides measured: 32 columns of
-// digits took 295 us for 16 sequences of 32K-64K tokens with groups of 32 heads, 78 us for 32 of
-// 1K-8K with two queries of 16 heads, where the f16 kernel takes 266 and 49; at 16 columns the
-// digits take 141 us and the f16 kernel 266 (groups of 16, 32K-64K tokens).
+// pays for no empty columns; beyond 16 the f16 kernel (0).  Both sides measured: at 16 columns the
+// digits take 143 us and the f16 kernel 210 (16 sequences of 32K-64K tokens, groups of 16); 32 columns
+// of digits took 295 us with groups of 32, and 78 us for 32 sequences of 1K-8K with two queries of 16
+// heads, where the f16 kernel takes 212 and 49.
 static int columns_of(int Hq, int Hk, int max_q) {
   const int64_t want = (int64_t)(Hq / Hk) * max_q;
   return want <= 8 ? 8 : want <= 16 ? 16 : 0;

@@ -130,7 +130,7 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// tanh in two parts.  Up to kTanhSmall an odd polynomial, x + x^3 q(x^2) with q fitted at Chebyshev
+// tanh by a series near zero and by the exponential beyond (tanh x = 1 - 2 / (1 + e^2x)).  Up to kTanhSmall an odd polynomial, x + x^3 q(x^2) with q fitted at Chebyshev
 // points: relative error 2^-26 and the roundings of its steps.  Beyond, 1 - 2 / (1 + e^2x): an
 // absolute error near 2^-22, which would be a relative 2^-17 of a score of a thirtieth of the cap.
 constexpr float kTanhSmall = 0.625f;

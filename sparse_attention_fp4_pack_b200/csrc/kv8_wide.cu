@@ -1,5 +1,5 @@
 // Attention over the paged 8-bit KV cache for many query rows per key head (chunks of prompts,
-// drafted tokens, large groups): csa2_kv8_attn's kernel from KvWide::kMinRows rows on.  The list
+// drafted tokens, large groups): csa2_kv8_attn's kernel beyond 16 rows (columns_of in kv8_attn.cu).  The list
 // of key tiles, its even split over the CTAs and the joining of split items are kv8_list.cuh's.
 //
 // With many rows a key tile is used often enough to pay for turning its E4M3 codes into f16
@@ -21,8 +21,8 @@
 //     are joined when the piece ends.
 // A softmax thread owns one row, so its maximum, sum and rescaling need no exchange.
 //
-// 8 x 64 drafts of 64 heads over 8K-32K keys take 440 us (900 TFLOP/s; 483 in long runs under the
-// 1000 W cap), chunks of 1024 rows 689 (885 TFLOP/s).  Of a slot's about 4000 cycles per key tile
+// 8 x 64 drafts of 64 heads over 8K-32K keys take 473 to 483 us (837 TFLOP/s; the 1000 W cap lowers the
+// clock), chunks of 1024 rows 684 to 689 (889 TFLOP/s).  Of a slot's about 4000 cycles per key tile
 // of 256 rows the softmax takes 2300 (maximum 750, exponentials 1000), its two products 1024, waits
 // and issue the rest; the tensor cores are busy 2048 of them.  With few rows the copies in flight
 // bound it (3.6 TB/s at 32 rows).
