@@ -42,10 +42,10 @@ struct KvAttnArgs {
   uint32_t* status;
 };
 
-// Partial results of CTA c (output over the piece's own sum, maximum, sum): slot 0 the piece that continues an item, slot 1 the one that
-// starts an item and does not end it.  meta: [0] slot 1 is used; then [1] the CTA whose slot 0
-// ends the item, [2] key head * head blocks + head block, [3] query block, [4] first row and
-// [5] number of queries of the request.
+// Partial results of CTA c, each an output over the piece's own sum, its maximum and its sum: slot 0
+// the piece that continues an item, slot 1 the one that starts an item and does not end it.  meta:
+// [0] slot 1 is used; then [1] the CTA whose slot 0 ends the item, [2] key head * head blocks + head
+// block, [3] query block, [4] first row and [5] number of queries of the request.
 constexpr int kMetaInts = 8;
 
 // Rows of hd bytes from `row` on (a box of the map) into shared memory.
@@ -130,9 +130,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// tanh by a series near zero and by the exponential beyond (tanh x = 1 - 2 / (1 + e^2x)).  Up to kTanhSmall an odd polynomial, x + x^3 q(x^2) with q fitted at Chebyshev
-// points: relative error 2^-26 and the roundings of its steps.  Beyond, 1 - 2 / (1 + e^2x): an
-// absolute error near 2^-22, which would be a relative 2^-17 of a score of a thirtieth of the cap.
+// tanh by an odd polynomial near zero and by the exponential beyond.  Up to kTanhSmall x + x^3 q(x^2)
+// with q fitted at Chebyshev points: relative error 2^-26 and the roundings of its steps.  Beyond,
+// 1 - 2 / (1 + e^2x): an absolute error near 2^-22, which would be a relative 2^-17 of a score of a
+// thirtieth of the cap.
 constexpr float kTanhSmall = 0.625f;
 constexpr float kTanh1 = -0.3333326280117035f, kTanh2 = 0.13331149518489838f, kTanh3 = -0.05372267961502075f,
                 kTanh4 = 0.020595679059624672f, kTanh5 = -0.005664775148034096f;
@@ -426,13 +427,13 @@ __device__ void find_share(const KvAttnArgs& a, const Shape& s, int64_t* sums, S
 }
 
 // Joins the pieces of the item that CTA blockIdx.x starts and does not end.  A piece left its own
-// output O (divided by its own sum l, so it is of the values' size whatever their scales), its
-// maximum m and l: with M the largest m and w = 2^(m - M) l, out = sum w O / sum w.  A warp joins one column: its
-// lanes first hold the statistics of 32 pieces, then 4 (2 of 64) channels each, so the loads of
+// output O (over its own sum l, so it is of the values' size whatever their scales), its maximum m
+// and l: with M the largest m and w = 2^(m - M) l, out = sum w O / sum w.  A warp joins one column:
+// its lanes first hold the statistics of 32 pieces, then 4 (2 of 64) channels each, so the loads of
 // all pieces are independent.
 constexpr int kMergeThreads = 256;  // 8 columns
-// Sums of weights reach 2^32 (2^30 keys of at most 2^2): 2^-34 keeps the weighted values, up to the
-// largest fp32, in range, and the smallest (2^-73, a scale of 2^-64) normal.
+// 2^24 keys of at most 2^10 (the larger of the kernels' slacks) sum up to 2^34: with 2^-34 the weighted
+// values stay in fp32 up to its largest, and the smallest (2^-73, a scale of 2^-64) normal.
 constexpr float kMergeShift = 34.0f;
 
 template <int NC, int HD, typename T>
